@@ -1,9 +1,9 @@
 """SegmentAttention for B200: Python binding of the C-ABI library ``libsegattn.so``.
 
 Every function here only marshals arguments for the C entry points declared
-in ``include/seg_attn.h`` (same names).  All compute runs in the library's
-sm_100a kernels; there is no fallback path.  PyTorch supplies device memory
-and streams only.
+in ``include/seg_attn.h``, ``include/seg_la.h`` and ``include/seg_draft.h`` (same
+names).  All compute runs in the library's sm_100a kernels; there is no fallback
+path.  PyTorch supplies device memory and streams only.
 """
 from __future__ import annotations
 
@@ -26,6 +26,10 @@ __all__ = [
     "seg_attn_decode_fp8", "seg_attn_prefill_fp8", "seg_attn_kv_append_fp8", "SHARE_PREFIX",
     "seg_la_table_desc", "seg_la_build_table", "seg_la_workspace_size", "seg_la_prefill",
     "seg_la_decode", "LATable",
+    "RopeScaling", "seg_attn_rope_desc", "seg_attn_rope_plan", "seg_attn_rope",
+    "seg_attn_rope_append", "seg_attn_rope_append_fp8", "seg_attn_tree_desc",
+    "seg_attn_build_tree_table", "seg_attn_tree_workspace_size", "seg_attn_tree",
+    "seg_attn_tree_fp8", "TreeTable", "seg_attn_kv_move",
 ]
 
 MODE_PREFILL = 0
@@ -83,6 +87,34 @@ class seg_la_table_desc(ctypes.Structure):
     ]
 
 
+class seg_attn_rope_scaling(ctypes.Structure):
+    """Mirror of ``seg_attn_rope_scaling`` in include/seg_draft.h."""
+    _fields_ = [
+        ("kind", ctypes.c_int32), ("num_factors", ctypes.c_int32), ("factor", ctypes.c_double),
+        ("original_len", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+        ("amp", ctypes.c_double), ("factors", ctypes.c_void_p),
+    ]
+
+
+class seg_attn_rope_desc(ctypes.Structure):
+    """Mirror of ``seg_attn_rope_desc`` in include/seg_draft.h."""
+    _fields_ = [("magic", ctypes.c_uint32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("amp", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * 128)]
+
+
+class seg_attn_tree_desc(ctypes.Structure):
+    """Mirror of ``seg_attn_tree_desc`` in include/seg_draft.h."""
+    _fields_ = [
+        ("magic", ctypes.c_uint32), ("version", ctypes.c_uint32),
+        ("batch", ctypes.c_int32), ("max_draft", ctypes.c_int32),
+        ("off_row", ctypes.c_int64), ("off_mask", ctypes.c_int64),
+        ("off_draft_slot", ctypes.c_int64), ("off_citem", ctypes.c_int64),
+        ("pass_", seg_attn_table_desc),
+        ("table_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64),
+    ]
+
+
 class seg_attn_pool_stats(ctypes.Structure):
     """Mirror of ``seg_attn_pool_stats`` in include/seg_attn.h."""
     _fields_ = [("num_slots", ctypes.c_int64), ("free_slots", ctypes.c_int64),
@@ -91,9 +123,10 @@ class seg_attn_pool_stats(ctypes.Structure):
 
 
 class SegAttnError(RuntimeError):
-    def __init__(self, fn: str, code: int):
+    def __init__(self, fn: str, code: int, detail: str = ""):
         self.code = code
-        super().__init__(f"{fn}: {seg_attn_status_string(code)} (status {code})")
+        super().__init__(f"{fn}: {seg_attn_status_string(code)} (status {code})"
+                         + (f": {detail}" if detail else ""))
 
 
 _lock = threading.Lock()
@@ -159,6 +192,24 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.seg_la_prefill.restype = I
         lib.seg_la_decode.argtypes = [P, P, P, P, P, P, P, LD, ctypes.c_float, P]
         lib.seg_la_decode.restype = I
+        RD, F = ctypes.POINTER(seg_attn_rope_desc), ctypes.c_float
+        TD = ctypes.POINTER(seg_attn_tree_desc)
+        lib.seg_attn_rope_plan.argtypes = [I, I, ctypes.c_double,
+                                           ctypes.POINTER(seg_attn_rope_scaling), RD]
+        lib.seg_attn_rope.argtypes = [P, I64, P, I64, P, I64, I, I, RD, I, P]
+        rows = [P, I64] * 4 + [P, P, I64, I, I, I, RD]
+        lib.seg_attn_rope_append.argtypes = rows + [P, P, I64, P]
+        lib.seg_attn_rope_append_fp8.argtypes = rows + [P, P, P, P, I64, P]
+        lib.seg_attn_build_tree_table.argtypes = [I, P, P, P, P, P, P, I64, I, I, I, P, SZ, TD]
+        lib.seg_attn_tree_workspace_size.argtypes = [TD]
+        lib.seg_attn_tree_workspace_size.restype = SZ
+        lib.seg_attn_tree.argtypes = [P, P, P, P, P, P, TD, F, P, SZ, P]
+        lib.seg_attn_tree_fp8.argtypes = [P, P, P, P, P, P, P, P, TD, F, P, SZ, P]
+        lib.seg_attn_kv_move.argtypes = [P, P, P, P, I64, P, I64, I, I, I, I64, P]
+        for fn in (lib.seg_attn_rope_plan, lib.seg_attn_rope, lib.seg_attn_rope_append,
+                   lib.seg_attn_rope_append_fp8, lib.seg_attn_build_tree_table,
+                   lib.seg_attn_tree, lib.seg_attn_tree_fp8, lib.seg_attn_kv_move):
+            fn.restype = I
         _lib = lib
         return lib
 
@@ -473,3 +524,264 @@ class LATable:
     @property
     def workspace_bytes(self) -> int:
         return seg_la_workspace_size(self.desc)
+
+
+# ------------------------------------------------- rotary positions and drafted tokens
+# These calls check dtypes, shapes, strides and devices as well, and run on the
+# tensors' device whichever is current (seg_draft.h has the rest of the contract).
+_ROPE_SCALES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4, "per_pair": 5}
+
+
+@dataclass
+class RopeScaling:
+    """Scaling of the rotary frequencies for contexts longer than the original one.
+
+    ``kind``: "linear", "ntk", "yarn", "wavelength" or "per_pair" (formulas in seg_draft.h);
+    ``amp`` 0 and ``low`` = ``high`` = 0 take the kind's own values; ``factors``: one per pair.
+    """
+    kind: str
+    factor: float = 1.0
+    original_len: float = 0.0
+    low: float = 0.0
+    high: float = 0.0
+    amp: float = 0.0
+    factors: Optional[Sequence[float]] = None
+
+
+def _bad(fn: str, detail: str):
+    raise SegAttnError(fn, STATUS["INVALID_ARG"], detail)
+
+
+def _invoke(fn_name: str, device: torch.device, stream, args: tuple) -> None:
+    """Call the entry point with ``args`` + the stream, with ``device`` current."""
+    fn = getattr(_lib or load_library(), fn_name)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        _bad(fn_name, f"stream on {stream.device}, tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != 0:
+        raise SegAttnError(fn_name, rc)
+
+
+def _ptr(fn: str, name: str, t: torch.Tensor, dtype, device, numel: Optional[int] = None) -> int:
+    """Address of a dense tensor of the given dtype, device and element count."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or (
+            numel is not None and t.numel() != numel):
+        _bad(fn, f"{name}: a dense {dtype} tensor on {device}"
+                 + (f" of {numel} values" if numel is not None else "")
+                 + f", not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(fn: str, name: str, t: torch.Tensor, n: int, heads: int, d: int, device):
+    """(address, token stride) of bf16 rows [n, heads, d] with dense heads."""
+    if (t.dtype is not torch.bfloat16 or t.device != device or tuple(t.shape) != (n, heads, d)
+            or (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)):
+        _bad(fn, f"{name}: bf16 [{n}, {heads}, {d}] with dense heads on {device}, "
+                 f"not {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _cuda_device(fn: str, name: str, t: torch.Tensor, dim: int) -> torch.device:
+    if not t.is_cuda or t.dim() != dim:
+        _bad(fn, f"{name}: a {dim}-dimensional CUDA tensor, not {t.dim()}-dimensional on {t.device}")
+    return t.device
+
+
+def seg_attn_rope_plan(rotary_dim: int, interleaved: bool = False, base: float = 10000.0,
+                       scaling: Optional[RopeScaling] = None) -> seg_attn_rope_desc:
+    """Plan of a rotation (host value, nothing to free).  Raises SegAttnError."""
+    desc, arg, keep = seg_attn_rope_desc(), None, None
+    if scaling is not None:
+        if scaling.kind not in _ROPE_SCALES:
+            _bad("seg_attn_rope_plan", f"scaling kind {scaling.kind!r}")
+        if scaling.factors is not None:
+            keep = np.ascontiguousarray(np.asarray(scaling.factors, dtype=np.float64).reshape(-1))
+        arg = ctypes.byref(seg_attn_rope_scaling(
+            _ROPE_SCALES[scaling.kind], keep.size if keep is not None else 0, scaling.factor,
+            scaling.original_len, scaling.low, scaling.high, scaling.amp,
+            keep.ctypes.data if keep is not None and keep.size else None))
+    rc = load_library().seg_attn_rope_plan(int(rotary_dim), int(bool(interleaved)), float(base),
+                                           arg, ctypes.byref(desc))
+    if rc != 0:
+        raise SegAttnError("seg_attn_rope_plan", rc)
+    return desc
+
+
+def seg_attn_rope(x, out, positions, rope: seg_attn_rope_desc, backward: bool = False,
+                  stream=None) -> None:
+    """Rotate x [n, heads, d] (bf16, dense heads, any token stride) into ``out`` (may be x) by
+    the angles of ``positions`` (device int32 [n]); ``backward``: the transposed rotation."""
+    fn = "seg_attn_rope"
+    dev = _cuda_device(fn, "x", x, 3)
+    n, h, d = x.shape
+    xp, xs = _rows(fn, "x", x, n, h, d, dev)
+    op, os_ = _rows(fn, "out", out, n, h, d, dev)
+    pos = _ptr(fn, "positions", positions, torch.int32, dev, n)
+    _invoke(fn, dev, stream, (xp, xs, op, os_, pos, n, h, d, ctypes.byref(rope), int(backward)))
+
+
+def _rope_append(fn, q, q_out, k_new, v_new, positions, slots, rope, scales, k_pool, v_pool,
+                 stream):
+    dev = _cuda_device(fn, "k_pool", k_pool, 3)
+    S, hk, d = k_pool.shape
+    n = k_new.shape[0]
+    if (q is None) != (q_out is None):
+        _bad(fn, "q and q_out: both or neither")
+    hq = q.shape[1] if q is not None else 0
+    rows = (_rows(fn, "q", q, n, hq, d, dev) + _rows(fn, "q_out", q_out, n, hq, d, dev)
+            if q is not None else (None, 0, None, 0))
+    rows += _rows(fn, "k_new", k_new, n, hk, d, dev) + _rows(fn, "v_new", v_new, n, hk, d, dev)
+    kind = torch.bfloat16 if scales is None else torch.uint8
+    args = rows + (_ptr(fn, "positions", positions, torch.int32, dev, n),
+                   _ptr(fn, "slots", slots, torch.int32, dev, n), n, hq, hk, d,
+                   ctypes.byref(rope))
+    if scales is not None:
+        args += tuple(_ptr(fn, "scales", t, torch.float32, dev, hk) for t in scales)
+    args += (_ptr(fn, "k_pool", k_pool, kind, dev), _ptr(fn, "v_pool", v_pool, kind, dev, S * hk * d),
+             S)
+    _invoke(fn, dev, stream, args)
+
+
+def seg_attn_rope_append(q, q_out, k_new, v_new, positions, slots, rope: seg_attn_rope_desc,
+                         k_pool, v_pool, stream=None) -> None:
+    """q_out = rotated q; rotated k_new and v_new into their ``slots`` of the bf16 pools.  q, k_new
+    and v_new [n, heads, d] may be parts of one projection; q and q_out may both be None."""
+    _rope_append("seg_attn_rope_append", q, q_out, k_new, v_new, positions, slots, rope, None,
+                 k_pool, v_pool, stream)
+
+
+def seg_attn_rope_append_fp8(q, q_out, k_new, v_new, positions, slots, rope: seg_attn_rope_desc,
+                             k_scale, v_scale, k_pool, v_pool, stream=None) -> None:
+    """seg_attn_rope_append into E4M3 pools (uint8) with per-kv-head fp32 scales."""
+    _rope_append("seg_attn_rope_append_fp8", q, q_out, k_new, v_new, positions, slots, rope,
+                 (k_scale, v_scale), k_pool, v_pool, stream)
+
+
+def seg_attn_build_tree_table(draft_lens, seg_counts, seg_starts, seg_lens, num_slots: int,
+                              q_heads: int, kv_heads: int, head_dim: int, parents=None, mask=None,
+                              pin: bool = False):
+    """Returns (host table as an int32 torch tensor, seg_attn_tree_desc).  Raises SegAttnError."""
+    fn = "seg_attn_build_tree_table"
+    lib = load_library()
+    dl, sc, ss, sl = _i32(draft_lens), _i32(seg_counts), _i32(seg_starts), _i32(seg_lens)
+    if sc.size != dl.size or int(np.maximum(sc, 0).sum(dtype=np.int64)) != ss.size or ss.size != sl.size:
+        _bad(fn, "seg_counts per request, seg_starts and seg_lens per segment")
+    pa = _i32(parents) if parents is not None else None
+    ma = None
+    if mask is not None:
+        ma = np.ascontiguousarray(np.asarray(mask).reshape(-1).astype(bool).view(np.uint8))
+    t = np.maximum(dl.astype(np.int64), 0)
+    if (pa is not None and pa.size != t.sum()) or (ma is not None and ma.size != (t * t).sum()):
+        _bad(fn, "parents: one per drafted token; mask: draft_len^2 per request")
+    desc = seg_attn_tree_desc()
+    # an empty parents or mask array still says which form the trees have
+    some = lambda a: None if a is None else ctypes.c_void_p(a.ctypes.data)
+    args = [int(dl.size), _np_ptr(dl), some(pa), some(ma), _np_ptr(sc), _np_ptr(ss), _np_ptr(sl),
+            int(num_slots), int(q_heads), int(kv_heads), int(head_dim)]
+    rc = lib.seg_attn_build_tree_table(*args, None, 0, ctypes.byref(desc))
+    if rc != 0:
+        raise SegAttnError(fn, rc)
+    host = torch.zeros(max(1, (desc.table_bytes + 3) // 4), dtype=torch.int32, pin_memory=pin)
+    rc = lib.seg_attn_build_tree_table(*args, ctypes.c_void_p(host.data_ptr()),
+                                       int(desc.table_bytes), ctypes.byref(desc))
+    if rc != 0:
+        raise SegAttnError(fn, rc)
+    return host, desc
+
+
+def seg_attn_tree_workspace_size(desc: seg_attn_tree_desc) -> int:
+    return int(load_library().seg_attn_tree_workspace_size(ctypes.byref(desc)))
+
+
+@dataclass
+class TreeTable:
+    """A built drafted-token table: host copy, description, device copy and workspace size."""
+    host: torch.Tensor
+    desc: seg_attn_tree_desc
+    device: Optional[torch.Tensor] = None
+
+    @classmethod
+    def build(cls, draft_lens, seg_starts, seg_lens, num_slots, q_heads, kv_heads, head_dim,
+              parents=None, mask=None, pin=False):
+        """Per-request segment lists in; ``parents`` / ``mask`` flat, requests back to back."""
+        host, desc = seg_attn_build_tree_table(
+            draft_lens, [len(s) for s in seg_starts], [x for s in seg_starts for x in s],
+            [x for s in seg_lens for x in s], num_slots, q_heads, kv_heads, head_dim,
+            parents=parents, mask=mask, pin=pin)
+        return cls(host=host, desc=desc)
+
+    def to(self, device, non_blocking=False) -> "TreeTable":
+        self.device = self.host.to(device, non_blocking=non_blocking)
+        return self
+
+    @property
+    def workspace_bytes(self) -> int:
+        return seg_attn_tree_workspace_size(self.desc)
+
+
+def _tree(fn, q, k_pool, v_pool, scales, out, lse, dev_table, desc, softmax_scale, workspace,
+          stream):
+    dev = _cuda_device(fn, "q", q, 3)
+    p = desc.pass_
+    n, hq, hk, d = p.total_q, p.q_heads, p.kv_heads, p.head_dim
+    kind = torch.bfloat16 if scales is None else torch.uint8
+    pool = p.num_slots * hk * d
+    args = (_ptr(fn, "q", q, torch.bfloat16, dev, n * hq * d),
+            _ptr(fn, "k_pool", k_pool, kind, dev, pool), _ptr(fn, "v_pool", v_pool, kind, dev, pool))
+    if scales is not None:
+        args += tuple(_ptr(fn, "scales", t, torch.float32, dev, hk) for t in scales)
+    args += (_ptr(fn, "out", out, torch.bfloat16, dev, n * hq * d),
+             _ptr(fn, "lse", lse, torch.float32, dev, n * hq) if lse is not None else None,
+             _ptr(fn, "dev_table", dev_table, torch.int32, dev), ctypes.byref(desc),
+             float(softmax_scale))
+    if dev_table.numel() * 4 < desc.table_bytes:
+        _bad(fn, "dev_table is shorter than the table")
+    if workspace is None:
+        args += (None, 0)
+    else:
+        args += (_ptr(fn, "workspace", workspace, workspace.dtype, dev), workspace.nbytes)
+    _invoke(fn, dev, stream, args)
+
+
+def seg_attn_tree(q, k_pool, v_pool, out, lse, dev_table, desc, softmax_scale, workspace=None,
+                  stream=None) -> None:
+    """Attention of drafted tokens (q, out bf16 [total, Hq, d]) over the bf16 pools; ``lse`` fp32
+    [total, Hq] or None."""
+    _tree("seg_attn_tree", q, k_pool, v_pool, None, out, lse, dev_table, desc, softmax_scale,
+          workspace, stream)
+
+
+def seg_attn_tree_fp8(q, k_pool, v_pool, k_scale, v_scale, out, lse, dev_table, desc,
+                      softmax_scale, workspace=None, stream=None) -> None:
+    """seg_attn_tree over E4M3 pools (uint8 [S, Hkv, d]) with per-kv-head fp32 scales."""
+    _tree("seg_attn_tree_fp8", q, k_pool, v_pool, (k_scale, v_scale), out, lse, dev_table, desc,
+          softmax_scale, workspace, stream)
+
+
+def seg_attn_kv_move(k_pool, v_pool, src, dst, offsets=None, stream=None) -> None:
+    """k_pool[dst[i]] = k_pool[src[i]], v_pool likewise (pools bf16 or uint8 [S, Hkv, d]; src, dst
+    device int32), in order inside each group ``offsets[g] : offsets[g + 1]`` (device int32;
+    None: every move on its own)."""
+    fn = "seg_attn_kv_move"
+    dev = _cuda_device(fn, "k_pool", k_pool, 3)
+    S, hk, d = k_pool.shape
+    kind = k_pool.dtype
+    if kind is not torch.bfloat16 and kind is not torch.uint8:
+        _bad(fn, f"k_pool: bfloat16 or uint8, not {kind}")
+    n = src.numel()
+    groups = 0
+    if offsets is not None:
+        groups = offsets.numel() - 1
+        if groups < 0:
+            _bad(fn, "offsets: at least one value")
+    args = (_ptr(fn, "k_pool", k_pool, kind, dev), _ptr(fn, "v_pool", v_pool, kind, dev, S * hk * d),
+            _ptr(fn, "src", src, torch.int32, dev, n), _ptr(fn, "dst", dst, torch.int32, dev, n), n,
+            _ptr(fn, "offsets", offsets, torch.int32, dev) if offsets is not None else None,
+            groups, hk, d, 2 if kind is torch.bfloat16 else 1, S)
+    _invoke(fn, dev, stream, args)

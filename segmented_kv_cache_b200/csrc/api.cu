@@ -229,9 +229,14 @@ extern "C" int seg_attn_take_device_error(int* value) {
   if (rc != SEG_ATTN_OK) return rc;
   rc = segattn::take_append_error(&append_err);
   if (rc != SEG_ATTN_OK) return rc;
+  int rope_err = 0, move_err = 0;
+  rc = segattn::take_rope_error(&rope_err);
+  if (rc != SEG_ATTN_OK) return rc;
+  rc = segattn::take_move_error(&move_err);
+  if (rc != SEG_ATTN_OK) return rc;
   int la_err = 0;
   rc = segla::take_la_error(&la_err);
   if (rc != SEG_ATTN_OK) return rc;
-  *value = (wait_err ? 1 : 0) | (append_err ? 2 : 0) | (la_err ? 4 : 0);
+  *value = (wait_err ? 1 : 0) | (append_err || rope_err || move_err ? 2 : 0) | (la_err ? 4 : 0);
   return SEG_ATTN_OK;
 }

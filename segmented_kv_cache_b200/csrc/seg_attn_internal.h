@@ -114,7 +114,7 @@ int launch_prefill(const PrefillLaunch& a, cudaStream_t stream);
 int launch_decode(const DecodeLaunch& a, cudaStream_t stream);
 
 // Read and clear the device error words: a bounded wait that gave up (prefill)
-// and a KV-append slot out of range.
+// and a slot out of range (KV append, rotated append, row move).
 int launch_wait_selftest(int wait_us, cudaStream_t stream);
 // Stall test of the prefill kernel (seg_attn_stall_test).
 int set_stall_test(int withhold_k_tile, int wait_us);
@@ -122,6 +122,8 @@ int set_stall_test(int withhold_k_tile, int wait_us);
 int set_order_test(int delay_ns);
 int take_device_error(int* value);
 int take_append_error(int* value);
+int take_rope_error(int* value);
+int take_move_error(int* value);
 
 // Workspace split of the decode call.
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

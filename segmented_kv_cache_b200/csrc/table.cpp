@@ -30,58 +30,10 @@
 #include <vector>
 
 #include "seg_attn.h"
+#include "plan.h"
 #include "seg_attn_internal.h"
 
-namespace {
-
-using segattn::align_up;
-using Row8 = std::array<int32_t, 8>;
-using Row4 = std::array<int32_t, 4>;
-// prefill piece: request, kv head, first query, first K tile | end K tile, partial
-// slot (-1: none), one-tile flag, end of the request's segments | first packed query
-// row, queries and keys of the request, segment holding the piece's first key | pool
-// slot of the piece's first key when its first K tile lies inside that segment (-1:
-// it does not), three zero words
-constexpr int kWorkInts = 16;
-using Row16 = std::array<int32_t, kWorkInts>;
-
-bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-
-struct Layout {
-  int64_t n = 0;  // int32 elements so far
-  int64_t take(int64_t count) {
-    int64_t at = n;
-    n += count;
-    n = (n + 3) / 4 * 4;  // every array starts 16-byte aligned
-    return at;
-  }
-};
-
-// A request's keys as a segment list (start, len) in logical order.
-struct Segs {
-  std::vector<int32_t> start, len;
-  int64_t keys() const {
-    int64_t k = 0;
-    for (int32_t l : len) k += l;
-    return k;
-  }
-};
-
-// Leading logical keys that two segment lists map to the same slots.
-int64_t common_prefix(const Segs& a, const Segs& b) {
-  size_t ia = 0, ib = 0;
-  int64_t oa = 0, ob = 0, n = 0;
-  for (;;) {
-    while (ia < a.len.size() && oa >= a.len[ia]) ++ia, oa = 0;
-    while (ib < b.len.size() && ob >= b.len[ib]) ++ib, ob = 0;
-    if (ia == a.len.size() || ib == b.len.size()) return n;
-    if ((int64_t)a.start[ia] + oa != (int64_t)b.start[ib] + ob) return n;
-    const int64_t step = std::min<int64_t>(a.len[ia] - oa, b.len[ib] - ob);
-    n += step;
-    oa += step;
-    ob += step;
-  }
-}
+namespace segattn {
 
 // Keys [from, from + count) of a segment list, as a segment list.
 Segs cut(const Segs& s, int64_t from, int64_t count) {
@@ -101,32 +53,16 @@ Segs cut(const Segs& s, int64_t from, int64_t count) {
   return out;
 }
 
-// One prefill item: (request, kv head, query tiles from q0) over `tiles` K tiles.
-// `cascade` items write every piece as a partial for the shared-prefix merge;
-// `single` items hold queries in their first 128-row query tile only.
-struct PItem {
-  int32_t r, g, q0, tiles;
-  bool cascade, single;
-};
-
-struct Pieces {
-  std::vector<Row16> work;      // two-tile pieces longest first, then single-tile ones
-  std::vector<Row8> merge;      // split items that are not cascade items
-  std::vector<int32_t> citem;   // per item: its index in `citems`, or -1
-  int32_t slots = 0;            // partial-result slots
-  int32_t single = 0;           // single-tile pieces (the tail of `work`)
-};
-
 // Cut items into pieces along their K tiles when that shortens the
 // longest-first schedule on the SMs.  Each CTA runs one piece; the schedule is
 // simulated by assigning pieces longest first to the least loaded SM (what the
 // block scheduler does with a grid in that order) and the split factor with the
 // shortest makespan wins (ties keep fewer splits).
 void plan_pieces(const std::vector<PItem>& items, int max_split, std::vector<Row4>& citems,
-                 Pieces& out) {
-  auto pieces_of = [](int32_t tiles, int f) {
-    if (f <= 1 || tiles < 2 * segattn::kMinPieceTiles) return 1;
-    return std::min(f, tiles / segattn::kMinPieceTiles);
+                 Pieces& out, int min_piece) {
+  auto pieces_of = [min_piece](int32_t tiles, int f) {
+    if (f <= 1 || tiles < 2 * min_piece) return 1;
+    return std::min(f, tiles / min_piece);
   };
   // Longest-first schedule of the pieces on the SMs (each piece costed at its K tiles
   // plus the per-piece start-up and epilogue), for a piece count per item.
@@ -169,12 +105,12 @@ void plan_pieces(const std::vector<PItem>& items, int max_split, std::vector<Row
     std::vector<int> c(items.size());
     for (size_t i = 0; i < items.size(); ++i) {
       const int32_t t = items[i].tiles;
-      if (t < 2 * segattn::kMinPieceTiles) {
+      if (t < 2 * min_piece) {
         c[i] = 1;
         continue;
       }
       const int want = (int)std::lround((double)t / len);
-      c[i] = std::max(1, std::min({want, max_split, (int)(t / segattn::kMinPieceTiles)}));
+      c[i] = std::max(1, std::min({want, max_split, (int)(t / min_piece)}));
     }
     cands.push_back(std::move(c));
   }
@@ -270,6 +206,28 @@ void fill_request_words(std::vector<Row16>& work, const std::vector<int32_t>& q_
       if (first_key + segattn::kTileKeys <= kstart_next && first_key >= ks)
         w[12] = (int32_t)(lists[r].start[local] + (first_key - ks));
     }
+  }
+}
+
+}  // namespace segattn
+
+namespace {
+
+using namespace segattn;
+
+// Leading logical keys that two segment lists map to the same slots.
+int64_t common_prefix(const Segs& a, const Segs& b) {
+  size_t ia = 0, ib = 0;
+  int64_t oa = 0, ob = 0, n = 0;
+  for (;;) {
+    while (ia < a.len.size() && oa >= a.len[ia]) ++ia, oa = 0;
+    while (ib < b.len.size() && ob >= b.len[ib]) ++ib, ob = 0;
+    if (ia == a.len.size() || ib == b.len.size()) return n;
+    if ((int64_t)a.start[ia] + oa != (int64_t)b.start[ib] + ob) return n;
+    const int64_t step = std::min<int64_t>(a.len[ia] - oa, b.len[ib] - ob);
+    n += step;
+    oa += step;
+    ob += step;
   }
 }
 

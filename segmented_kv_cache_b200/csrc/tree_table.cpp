@@ -1,0 +1,242 @@
+// Host side of the drafted-token attention: validator, mask words and work plan.
+//
+// The pass over the cached keys is the prefill kernel run without a causal mask
+// on each request's first P keys, every piece writing a partial, exactly as the
+// pass over shared prefixes is; the drafted tokens' own keys, of which a token
+// sees a handful, are left to the kernel that joins the partials (tree.cu).
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <limits>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "plan.h"
+#include "seg_attn_internal.h"
+#include "seg_draft.h"
+
+namespace {
+
+using namespace segattn;
+
+int build(int batch, const int32_t* draft_lens, const int32_t* parents, const uint8_t* mask,
+          const int32_t* seg_counts, const int32_t* seg_starts, const int32_t* seg_lens,
+          int64_t num_slots, int q_heads, int kv_heads, int head_dim, void* host_out,
+          size_t host_out_bytes, seg_attn_tree_desc* desc) {
+  if (batch < 0 || num_slots < 0 || (parents && mask)) return SEG_ATTN_ERR_INVALID_ARG;
+  if (q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0) return SEG_ATTN_ERR_INVALID_ARG;
+  if (batch > 0 && (!seg_counts || !draft_lens)) return SEG_ATTN_ERR_INVALID_ARG;
+  const int group = q_heads / kv_heads;
+  if (head_dim != 64 && head_dim != 128) return SEG_ATTN_ERR_UNSUPPORTED;
+  if (!is_pow2(group) || group > kTileRows) return SEG_ATTN_ERR_UNSUPPORTED;
+  const int64_t kI32Max = std::numeric_limits<int32_t>::max();
+  // the K/V gather addresses pool rows (slot * kv_heads + head) with int32
+  if (num_slots > kI32Max / kv_heads) return SEG_ATTN_ERR_UNSUPPORTED;
+  int64_t nseg_in = 0;
+  for (int r = 0; r < batch; ++r) {
+    if (seg_counts[r] < 0) return SEG_ATTN_ERR_INVALID_ARG;
+    nseg_in += seg_counts[r];
+  }
+  if (nseg_in > kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
+  if (nseg_in > 0 && (!seg_starts || !seg_lens)) return SEG_ATTN_ERR_INVALID_ARG;
+
+  std::vector<int32_t> q_off(batch + 1, 0), prior(batch), draft_slot;
+  std::vector<Segs> own(batch);
+  std::vector<uint32_t> words;            // mask words, rows back to back
+  std::vector<int64_t> mask_at(batch);    // first word of each request
+  int64_t total_q = 0, total_k = 0, seg0 = 0, mask0 = 0, nseg = 0;
+  int32_t max_draft = 0;
+  std::vector<std::pair<int64_t, int64_t>> runs;
+  for (int r = 0; r < batch; ++r) {
+    Segs all;
+    int64_t k = 0;
+    runs.clear();
+    for (int s = 0; s < seg_counts[r]; ++s) {
+      const int64_t st = seg_starts[seg0 + s], ln = seg_lens[seg0 + s];
+      if (ln < 0) return SEG_ATTN_ERR_INVALID_ARG;
+      if (st < 0 || st + ln > num_slots) return SEG_ATTN_ERR_SEGMENT_OOB;
+      k += ln;
+      if (ln > 0) runs.emplace_back(st, ln);
+      all.start.push_back((int32_t)st);
+      all.len.push_back((int32_t)ln);
+    }
+    seg0 += seg_counts[r];
+    std::sort(runs.begin(), runs.end());
+    for (size_t i = 1; i < runs.size(); ++i)
+      if (runs[i].first < runs[i - 1].first + runs[i - 1].second)
+        return SEG_ATTN_ERR_SEGMENT_OVERLAP;
+    if (k > kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
+    const int32_t t = draft_lens[r];
+    if (t < 0) return SEG_ATTN_ERR_INVALID_ARG;
+    if (t > SEG_ATTN_TREE_MAX_DRAFT) return SEG_ATTN_ERR_UNSUPPORTED;
+    if (t > k) return SEG_ATTN_ERR_QLEN_GT_KLEN;
+    prior[r] = (int32_t)(k - t);
+    own[r] = cut(all, 0, k - t);
+    nseg += (int64_t)own[r].len.size();
+    const Segs drafts = cut(all, k - t, t);
+    for (size_t i = 0; i < drafts.len.size(); ++i)
+      for (int32_t j = 0; j < drafts.len[i]; ++j) draft_slot.push_back(drafts.start[i] + j);
+    // mask rows
+    const int32_t nw = (t + 31) / 32;
+    mask_at[r] = (int64_t)words.size();
+    words.resize(words.size() + (size_t)t * nw, 0u);
+    uint32_t* rows = words.data() + mask_at[r];
+    for (int32_t i = 0; i < t; ++i) {
+      uint32_t* row = rows + (size_t)i * nw;
+      if (mask) {
+        const uint8_t* m = mask + mask0 + (int64_t)i * t;
+        for (int32_t j = 0; j < t; ++j)
+          if (m[j]) row[j >> 5] |= 1u << (j & 31);
+        continue;
+      }
+      const int32_t p = parents ? parents[total_q + i] : i - 1;
+      if (p < -1 || p >= i) return SEG_ATTN_ERR_INVALID_ARG;
+      if (p >= 0)
+        for (int32_t w = 0; w < nw; ++w) row[w] = rows[(size_t)p * nw + w];
+      row[i >> 5] |= 1u << (i & 31);
+    }
+    mask0 += (int64_t)t * t;
+    total_q += t;
+    total_k += prior[r];
+    if (total_q > kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
+    q_off[r + 1] = (int32_t)total_q;
+    max_draft = std::max(max_draft, t);
+  }
+
+  // ---- the pass over the cached keys
+  const int32_t qpt = kTileRows / group;
+  const int32_t span = qpt * kTilesPerItem;
+  std::vector<PItem> items;
+  std::vector<int64_t> item0(batch, -1);
+  int32_t max_k_tiles = 0;
+  for (int r = 0; r < batch; ++r) {
+    const int32_t t = q_off[r + 1] - q_off[r];
+    if (prior[r] == 0 || t == 0) continue;
+    item0[r] = (int64_t)items.size();
+    const int32_t tiles = (int32_t)(((int64_t)prior[r] + kTileKeys - 1) / kTileKeys);
+    max_k_tiles = std::max(max_k_tiles, tiles);
+    for (int32_t q0 = 0; q0 < t; q0 += span)
+      for (int g = 0; g < kv_heads; ++g) items.push_back({r, g, q0, tiles, true, t - q0 <= qpt});
+  }
+  // few items are cut finely enough to give every SM a few pieces
+  const int max_split =
+      items.empty() ? 1
+                    : (int)std::max<int64_t>(kMaxSplit, 2 * kSmCount / (int64_t)items.size());
+  std::vector<Row4> citems;
+  Pieces pieces;
+  plan_pieces(items, max_split, citems, pieces);
+  if (pieces.work.size() > (size_t)kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
+
+  // ---- layout
+  Layout lay;
+  seg_attn_table_desc& p = desc->pass;
+  p.off_q_offsets = lay.take(batch + 1);
+  p.off_k_lens = lay.take(batch);
+  p.off_seg_offsets = lay.take(batch + 1);
+  p.off_seg_start = lay.take(nseg);
+  p.off_seg_kstart = lay.take(nseg);
+  p.off_seg_len = lay.take(nseg);
+  p.off_work = lay.take(kWorkInts * (int64_t)pieces.work.size());
+  desc->off_row = lay.take(8 * total_q);
+  desc->off_mask = lay.take((int64_t)words.size());
+  desc->off_draft_slot = lay.take(total_q);
+  desc->off_citem = lay.take(4 * (int64_t)citems.size());
+
+  p.magic = SEG_ATTN_TABLE_MAGIC;
+  p.version = SEG_ATTN_TABLE_VERSION;
+  p.mode = SEG_ATTN_MODE_PREFILL;
+  p.batch = batch;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.head_dim = head_dim;
+  p.num_slots = num_slots;
+  p.total_q = total_q;
+  p.total_k = total_k;
+  p.num_segments = (int32_t)nseg;
+  p.num_work = (int32_t)pieces.work.size();
+  p.queries_per_tile = qpt;
+  p.max_k_tiles = max_k_tiles;
+  p.num_parts = pieces.slots;
+  p.num_single = pieces.single;
+  desc->magic = SEG_ATTN_TREE_MAGIC;
+  desc->version = SEG_ATTN_TREE_VERSION;
+  desc->batch = batch;
+  desc->max_draft = max_draft;
+  desc->table_bytes = (uint64_t)lay.n * sizeof(int32_t);
+  desc->workspace_bytes = workspace_layout(p, false).total;
+  p.table_bytes = desc->table_bytes;
+  p.workspace_bytes = desc->workspace_bytes;
+
+  if (!host_out) return SEG_ATTN_OK;  // size query
+  if (host_out_bytes < desc->table_bytes) return SEG_ATTN_ERR_BUFFER_TOO_SMALL;
+  if ((reinterpret_cast<uintptr_t>(host_out) & 15) != 0) return SEG_ATTN_ERR_INVALID_ARG;
+
+  int32_t* t = static_cast<int32_t*>(host_out);
+  memset(t, 0, desc->table_bytes);
+  memcpy(t + p.off_q_offsets, q_off.data(), q_off.size() * sizeof(int32_t));
+  std::vector<int32_t> seg_off(batch + 1, 0);
+  int32_t s0 = 0;
+  for (int r = 0; r < batch; ++r) {
+    t[p.off_k_lens + r] = prior[r];
+    int32_t logical = 0;
+    for (size_t s = 0; s < own[r].len.size(); ++s, ++s0) {
+      t[p.off_seg_start + s0] = own[r].start[s];
+      t[p.off_seg_kstart + s0] = logical;
+      t[p.off_seg_len + s0] = own[r].len[s];
+      logical += own[r].len[s];
+    }
+    seg_off[r + 1] = s0;
+    t[p.off_seg_offsets + r + 1] = s0;
+    const int32_t n = q_off[r + 1] - q_off[r], nw = (n + 31) / 32;
+    for (int32_t i = 0; i < n; ++i) {
+      int32_t* row = t + desc->off_row + 8 * ((int64_t)q_off[r] + i);
+      const int64_t at = desc->off_mask + mask_at[r] + (int64_t)i * nw;
+      row[0] = q_off[r];
+      row[1] = nw;
+      row[2] = (int32_t)(uint32_t)(at & 0xffffffff);
+      row[3] = (int32_t)(at >> 32);
+      const int32_t block = i / span, local = i - block * span;
+      row[4] = item0[r] < 0 ? -1 : pieces.citem[item0[r] + (int64_t)block * kv_heads];
+      row[5] = (local / qpt) * kTileRows + (local % qpt) * group;
+    }
+  }
+  fill_request_words(pieces.work, q_off, prior, own, seg_off);
+  for (size_t i = 0; i < pieces.work.size(); ++i)
+    memcpy(t + p.off_work + kWorkInts * i, pieces.work[i].data(), kWorkInts * sizeof(int32_t));
+  if (!words.empty()) memcpy(t + desc->off_mask, words.data(), words.size() * sizeof(uint32_t));
+  if (!draft_slot.empty())
+    memcpy(t + desc->off_draft_slot, draft_slot.data(), draft_slot.size() * sizeof(int32_t));
+  for (size_t i = 0; i < citems.size(); ++i)
+    memcpy(t + desc->off_citem + 4 * i, citems[i].data(), 4 * sizeof(int32_t));
+  return SEG_ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" int seg_attn_build_tree_table(int batch, const int32_t* draft_lens,
+                                         const int32_t* parents, const uint8_t* mask,
+                                         const int32_t* seg_counts, const int32_t* seg_starts,
+                                         const int32_t* seg_lens, int64_t num_slots, int q_heads,
+                                         int kv_heads, int head_dim, void* host_out,
+                                         size_t host_out_bytes, seg_attn_tree_desc* desc) {
+  if (!desc) return SEG_ATTN_ERR_INVALID_ARG;
+  memset(desc, 0, sizeof(*desc));
+  int rc;
+  try {
+    rc = build(batch, draft_lens, parents, mask, seg_counts, seg_starts, seg_lens, num_slots,
+               q_heads, kv_heads, head_dim, host_out, host_out_bytes, desc);
+  } catch (const std::exception&) {  // host memory: no exception leaves a C entry
+    rc = SEG_ATTN_ERR_UNSUPPORTED;
+  }
+  // a failed build leaves nothing a compute call would accept; a too small buffer
+  // leaves the needed size
+  if (rc != SEG_ATTN_OK) desc->magic = 0;
+  return rc;
+}
+
+extern "C" size_t seg_attn_tree_workspace_size(const seg_attn_tree_desc* desc) {
+  if (!desc || desc->magic != SEG_ATTN_TREE_MAGIC) return 0;
+  return (size_t)desc->workspace_bytes;
+}

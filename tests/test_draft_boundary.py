@@ -1,0 +1,304 @@
+"""Rotary plans, tree tables and argument checks of the drafted-token calls (no GPU)."""
+import ctypes
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import segmented_kv_cache_b200 as sa
+from segmented_kv_cache_b200 import _build
+
+import draft_reference as ref
+
+S = sa.STATUS
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    _build.build()
+    return sa.load_library()
+
+
+def code_of(fn):
+    with pytest.raises(sa.SegAttnError) as e:
+        fn()
+    return e.value.code
+
+
+# ------------------------------------------------------------------------ rotary plans
+def turns(desc):
+    return [int(desc.turns[i]) for i in range(desc.rotary_dim // 2)]
+
+
+def same_frequencies(desc, inv_freq):
+    """Turn fractions against 64-bit frequencies: a double's 2^-53 and half a unit of 2^-64."""
+    for t, w in zip(turns(desc), inv_freq):
+        want = w / (2 * math.pi)
+        want -= math.floor(want)
+        assert abs(t / 2.0 ** 64 - want) <= 4 * 2.0 ** -53 * max(want, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("rotary", [2, 20, 64, 128, 256])
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 1.5])
+def test_plain_plan(rotary, base):
+    d = sa.seg_attn_rope_plan(rotary, base=base)
+    assert d.rotary_dim == rotary and d.layout == 0 and d.amp == 1.0
+    same_frequencies(d, ref.plain_freq(rotary, base))
+    assert sa.seg_attn_rope_plan(rotary, interleaved=True).layout == 1
+
+
+def test_scalings():
+    r, base, f, L = 64, 10000.0, 8.0, 4096
+    w = ref.plain_freq(r, base)
+    plan = lambda **kw: sa.seg_attn_rope_plan(r, base=base, scaling=sa.RopeScaling(**kw))
+    same_frequencies(plan(kind="none"), w)
+    same_frequencies(plan(kind="linear", factor=f), [x / f for x in w])
+    same_frequencies(plan(kind="ntk", factor=f), ref.plain_freq(r, base * f ** (r / (r - 2))))
+    d = plan(kind="per_pair", factors=[1 + i for i in range(r // 2)])
+    same_frequencies(d, [x / (1 + i) for i, x in enumerate(w)])
+    # the ends of the blends keep or divide the frequency, and it falls in between
+    for kind, high in (("yarn", 32.0), ("wavelength", 4.0)):
+        d = plan(kind=kind, factor=f, original_len=L)
+        got = [t / 2.0 ** 64 * 2 * math.pi for t in turns(d)]
+        ratio = [g / x for g, x in zip(got, w)]
+        assert ratio[0] == pytest.approx(1.0) and ratio[-1] == pytest.approx(1 / f)
+        assert all(a >= b - 1e-12 for a, b in zip(ratio, ratio[1:]))
+        e = plan(kind=kind, factor=f, original_len=L, low=1.0, high=high)
+        assert turns(e) == turns(d)
+    assert plan(kind="yarn", factor=f, original_len=L).amp == pytest.approx(0.1 * math.log(f) + 1)
+    assert plan(kind="yarn", factor=f, original_len=L, amp=1.25).amp == 1.25
+    assert plan(kind="linear", factor=f, amp=0.5).amp == 0.5
+    # wavelength: k_i at a pair in the blend, by the formula
+    d = plan(kind="wavelength", factor=f, original_len=L)
+    for i, x in enumerate(w):
+        k = min(max((L * x / (2 * math.pi) - 1) / 3, 0), 1)
+        assert turns(d)[i] / 2.0 ** 64 * 2 * math.pi == pytest.approx(x * k + x / f * (1 - k), rel=1e-12)
+
+
+def test_plan_refusals():
+    plan = sa.seg_attn_rope_plan
+    for r in (0, -2, 3, 258):
+        assert code_of(lambda: plan(r)) == S["UNSUPPORTED"]
+    for base in (1.0, 0.0, -3.0, math.inf, math.nan):
+        assert code_of(lambda: plan(64, base=base)) == S["INVALID_ARG"]
+    R = sa.RopeScaling
+    for sc in (R("linear", factor=0.0), R("linear", factor=math.nan), R("ntk", factor=-1.0),
+               R("yarn", factor=2.0), R("yarn", factor=2.0, original_len=-5),
+               R("wavelength", factor=2.0, original_len=100, low=4.0, high=4.0),
+               R("wavelength", factor=2.0, original_len=100, low=4.0, high=1.0),
+               R("per_pair"), R("per_pair", factors=[1.0] * 31), R("per_pair", factors=[0.0] * 32),
+               R("linear", factor=2.0, amp=-1.0), R("bent")):
+        assert code_of(lambda: plan(64, scaling=sc)) == S["INVALID_ARG"], sc
+    assert sa.load_library().seg_attn_rope_plan(64, 2, 1e4, None, ctypes.byref(
+        sa.seg_attn_rope_desc())) == S["INVALID_ARG"]
+    assert sa.load_library().seg_attn_rope_plan(64, 0, 1e4, None, None) == S["INVALID_ARG"]
+
+
+# ------------------------------------------------------------------------ tree tables
+def build(draft, segs, num_slots=4000, hq=8, hkv=2, d=128, **kw):
+    return sa.TreeTable.build(draft, [[s for s, _ in r] for r in segs],
+                              [[l for _, l in r] for r in segs], num_slots, hq, hkv, d, **kw)
+
+
+def test_tree_table_refusals():
+    ok = [[(0, 10), (100, 20)]]
+    build([5], ok)
+    assert code_of(lambda: build([5], [[(3995, 10)]])) == S["SEGMENT_OOB"]
+    assert code_of(lambda: build([5], [[(-1, 10)]])) == S["SEGMENT_OOB"]
+    assert code_of(lambda: build([5], [[(0, 10), (5, 10)]])) == S["SEGMENT_OVERLAP"]
+    assert code_of(lambda: build([31], ok)) == S["QLEN_GT_KLEN"]
+    assert code_of(lambda: build([-1], ok)) == S["INVALID_ARG"]
+    assert code_of(lambda: build([5], [[(0, -1)]])) == S["INVALID_ARG"]
+    assert code_of(lambda: build([1025], [[(0, 3000)]])) == S["UNSUPPORTED"]
+    build([1024], [[(0, 3000)]])
+    for parents in ([0, 0, 1, 2, 3], [-1, 1, 1, 2, 3], [-2, 0, 0, 0, 0], [-1, 5, 0, 0, 0]):
+        assert code_of(lambda: build([5], ok, parents=parents)) == S["INVALID_ARG"]
+    assert code_of(lambda: build([5], ok, parents=[-1] * 4)) == S["INVALID_ARG"]
+    assert code_of(lambda: build([5], ok, mask=[1] * 24)) == S["INVALID_ARG"]
+    assert code_of(lambda: build([5], ok, parents=[-1] * 5, mask=[1] * 25)) == S["INVALID_ARG"]
+    assert code_of(lambda: build([5], ok, d=96)) == S["UNSUPPORTED"]
+    assert code_of(lambda: build([5], ok, hq=6, hkv=2)) == S["UNSUPPORTED"]
+    assert code_of(lambda: build([5], ok, hq=6, hkv=4)) == S["INVALID_ARG"]
+    assert code_of(lambda: build([5], ok, hq=256, hkv=1)) == S["UNSUPPORTED"]
+    assert code_of(lambda: build([5, 5], ok)) == S["INVALID_ARG"]
+    assert code_of(lambda: build([1], [[(0, 5)]], num_slots=1 << 31, hq=2, hkv=1)) == S["UNSUPPORTED"]
+    # a pool that only just fits the row index, and one past it
+    build([1], [[(0, 5)]], num_slots=(1 << 31) // 2 - 1, hq=2, hkv=2)
+    assert code_of(lambda: build([1], [[(0, 5)]], num_slots=1 << 30, hq=2, hkv=2)) == S["UNSUPPORTED"]
+
+
+def test_small_buffer_and_null_desc(lib):
+    P = ctypes.c_void_p
+    i32 = lambda x: np.array(x, dtype=np.int32)
+    dl, sc, ss, sl = i32([3]), i32([1]), i32([0]), i32([200])
+    desc = sa.seg_attn_tree_desc()
+    args = [1, P(dl.ctypes.data), None, None, P(sc.ctypes.data), P(ss.ctypes.data),
+            P(sl.ctypes.data), 300, 4, 2, 64]
+    assert lib.seg_attn_build_tree_table(*args, None, 0, None) == S["INVALID_ARG"]
+    assert lib.seg_attn_build_tree_table(*args, None, 0, ctypes.byref(desc)) == 0
+    need = desc.table_bytes
+    buf = np.zeros(need // 4 + 8, dtype=np.int32)
+    at = (-buf.ctypes.data) % 16 + buf.ctypes.data
+    assert lib.seg_attn_build_tree_table(*args, P(at), need - 4, ctypes.byref(desc)) == \
+        S["BUFFER_TOO_SMALL"]
+    assert desc.table_bytes == need and lib.seg_attn_tree_workspace_size(ctypes.byref(desc)) == 0
+    assert lib.seg_attn_build_tree_table(*args, P(at + 4), need, ctypes.byref(desc)) == S["INVALID_ARG"]
+    assert lib.seg_attn_build_tree_table(*args, P(at), need, ctypes.byref(desc)) == 0
+
+
+def words_of(tab, n):
+    d = tab.desc
+    return tab.host[d.off_row: d.off_row + 8 * n].view(-1, 8).tolist()
+
+
+@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (64, 8), (128, 1), (3, 3)])
+def test_tree_table_content(seed, hq, hkv):
+    rnd = random.Random(seed)
+    B = rnd.randint(1, 6)
+    draft = [rnd.choice([0, 1, 2, 31, 32, 33, 70, 300]) for _ in range(B)]
+    prior = [rnd.choice([0, 1, 127, 128, 129, 3000]) for _ in range(B)]
+    c = ref.tree_case(rnd, draft, prior, hq, hkv, 64, device="cpu")
+    form = seed % 3
+    kw = {}
+    if form == 0:
+        kw = dict(parents=[p for t in draft for p in ref.random_parents(rnd, t)])
+    elif form == 1:
+        kw = dict(mask=[rnd.random() < 0.3 for _ in range(sum(t * t for t in draft))])
+    tab = sa.TreeTable.build(draft, c["seg_starts"], c["seg_lens"], c["num_slots"], hq, hkv, 64, **kw)
+    vis = ref.visible(draft, **kw)
+    d, p, host = tab.desc, tab.desc.pass_, tab.host
+    rows = words_of(tab, sum(draft))
+    slot = host[d.off_draft_slot: d.off_draft_slot + sum(draft)].tolist()
+    G = hq // hkv
+    qpt = 128 // G
+    work = host[p.off_work: p.off_work + 16 * p.num_work].view(-1, 16).tolist()
+    pieces = {}
+    for w in work:
+        pieces.setdefault((w[0], w[1], w[2]), []).append((w[5], w[3], w[4]))
+    seen_slots, at = [], 0
+    for r, t in enumerate(draft):
+        keys = [s + i for s, l in zip(c["seg_starts"][r], c["seg_lens"][r]) for i in range(l)]
+        assert slot[at:at + t] == keys[prior[r]:]
+        for i in range(t):
+            w = rows[at + i]
+            assert w[0] == at and w[1] == (t + 31) // 32
+            m0 = (w[2] & 0xffffffff) | (w[3] << 32)
+            bits = [x & 0xffffffff for x in host[m0:m0 + w[1]].tolist()]
+            assert [bool(bits[j >> 5] >> (j & 31) & 1) for j in range(t)] == vis[r][i].tolist()
+            if prior[r] == 0:
+                assert w[4] == -1
+                continue
+            block, local = divmod(i, 2 * qpt)
+            assert w[5] == (local // qpt) * 128 + (local % qpt) * G
+            for g in range(hkv):
+                slot0, n, q0, _ = host[d.off_citem + 4 * (w[4] + g):][:4].tolist()
+                assert q0 == block * 2 * qpt
+                # the item's pieces: consecutive slots over all of its K tiles
+                got = sorted(pieces[(r, g, q0)])
+                assert [x[0] for x in got] == list(range(slot0, slot0 + n))
+                assert got[0][1] == 0 and got[-1][2] == (prior[r] + 127) // 128
+                assert all(a[2] == b[1] for a, b in zip(got, got[1:]))
+                seen_slots += [x[0] for x in got] if local == 0 else []
+        at += t
+    assert sorted(seen_slots) == list(range(p.num_parts)) and p.num_parts == p.num_work
+    if p.num_work:
+        assert tab.workspace_bytes >= p.num_parts * 256 * (64 + 1) * 4
+
+
+def test_empty_batches():
+    tab = sa.TreeTable.build([], [], [], 10, 4, 2, 64)
+    assert tab.desc.pass_.total_q == 0 and tab.workspace_bytes == 0
+    tab = build([0, 0], [[(0, 10)], []])
+    assert tab.desc.pass_.num_work == 0
+
+
+# ------------------------------------------------------------------------ call refusals
+def test_compute_refusals_before_any_launch(lib):
+    """Every bad argument is answered on the host (fake addresses: nothing is launched)."""
+    A, U = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 1)
+    rope = sa.seg_attn_rope_plan(64)
+    R = ctypes.byref(rope)
+    f = lib.seg_attn_rope
+    I = S["INVALID_ARG"]
+    assert f(None, 512, A, 512, A, 2, 4, 128, R, 0, None) == I
+    assert f(A, 512, None, 512, A, 2, 4, 128, R, 0, None) == I
+    assert f(U, 512, A, 512, A, 2, 4, 128, R, 0, None) == I
+    assert f(A, 512, A, 512, None, 2, 4, 128, R, 0, None) == I
+    assert f(A, 511, A, 512, A, 2, 4, 128, R, 0, None) == I
+    assert f(A, 512, A, 0, A, 2, 4, 128, R, 0, None) == I
+    assert f(A, 512, A, 512, A, -1, 4, 128, R, 0, None) == I
+    assert f(A, 512, A, 512, A, 2, 0, 128, R, 0, None) == I
+    assert f(A, 512, A, 512, A, 2, 4, 62, R, 0, None) == I
+    assert f(A, 512, A, 512, A, 2, 4, 128, R, 2, None) == I
+    assert f(A, 512, A, 512, A, 2, 4, 128, None, 0, None) == I
+    assert f(A, 512, A, 512, A, 2, 4, 128, ctypes.byref(sa.seg_attn_rope_desc()), 0, None) == I
+    assert f(A, 1 << 20, A, 1 << 20, A, 2, 4, 8192, R, 0, None) == S["UNSUPPORTED"]
+    assert f(None, 0, None, 0, None, 0, 4, 128, R, 0, None) == 0
+
+    def append(q=A, qo=A, k=A, v=A, pos=A, slots=A, n=2, hq=4, hk=2, d=128, kp=A, vp=A, S_=10,
+               st=(512, 512, 256, 256)):
+        return lib.seg_attn_rope_append(q, st[0], qo, st[1], k, st[2], v, st[3], pos, slots, n, hq,
+                                        hk, d, R, kp, vp, S_, None)
+    for kw in (dict(q=None), dict(qo=None), dict(k=None), dict(v=None), dict(pos=None),
+               dict(slots=None), dict(kp=None), dict(vp=None), dict(n=-1), dict(hq=-1), dict(hk=0),
+               dict(S_=-1), dict(d=32), dict(st=(511, 512, 256, 256)), dict(st=(512, 512, 255, 256)),
+               dict(st=(512, 512, 256, 0)), dict(slots=U)):
+        assert append(**kw) == I, kw
+    assert append(n=0, q=None, k=None) == 0
+    assert lib.seg_attn_rope_append_fp8(A, 512, A, 512, A, 256, A, 256, A, A, 2, 4, 2, 128, R, None, A,
+                                        A, A, 10, None) == I
+
+    g = lib.seg_attn_kv_move
+    assert g(None, A, A, A, 3, None, 0, 2, 64, 2, 10, None) == I
+    assert g(A, U, A, A, 3, None, 0, 2, 64, 2, 10, None) == I
+    assert g(A, A, None, A, 3, None, 0, 2, 64, 2, 10, None) == I
+    assert g(A, A, A, U, 3, None, 0, 2, 64, 2, 10, None) == I
+    assert g(A, A, A, A, -1, None, 0, 2, 64, 2, 10, None) == I
+    assert g(A, A, A, A, 3, A, -1, 2, 64, 2, 10, None) == I
+    assert g(A, A, A, A, 3, None, 0, 2, 64, 4, 10, None) == I
+    assert g(A, A, A, A, 3, None, 0, 0, 64, 2, 10, None) == I
+    assert g(A, A, A, A, 3, None, 0, 2, 64, 2, -1, None) == I
+    assert g(A, A, A, A, 3, None, 0, 1, 12, 2, 10, None) == S["UNSUPPORTED"]
+    assert g(A, A, A, A, 0, None, 0, 2, 64, 2, 10, None) == 0
+    assert g(A, A, A, A, 3, A, 0, 2, 64, 2, 10, None) == 0
+
+    tab = build([3], [[(0, 500)]])
+    D = ctypes.byref(tab.desc)
+    h = lib.seg_attn_tree
+    assert tab.workspace_bytes > 0
+    ws = tab.workspace_bytes
+    assert h(None, A, A, A, A, A, D, 0.1, A, ws, None) == I
+    assert h(A, None, A, A, A, A, D, 0.1, A, ws, None) == I
+    assert h(A, A, A, U, A, A, D, 0.1, A, ws, None) == I
+    assert h(A, A, A, A, U, A, D, 0.1, A, ws, None) == I
+    assert h(A, A, A, A, A, None, D, 0.1, A, ws, None) == I
+    assert h(A, A, A, A, A, A, None, 0.1, A, ws, None) == I
+    for s in (0.0, -1.0, math.inf, math.nan):
+        assert h(A, A, A, A, A, A, D, s, A, ws, None) == I
+    assert h(A, A, A, A, A, A, D, 0.1, None, 0, None) == S["WORKSPACE"]
+    assert h(A, A, A, A, A, A, D, 0.1, A, ws - 1, None) == S["WORKSPACE"]
+    assert h(A, A, A, A, A, A, D, 0.1, U, ws, None) == S["WORKSPACE"]
+    assert lib.seg_attn_tree_fp8(A, A, A, None, A, A, A, A, D, 0.1, A, ws, None) == I
+    bad = sa.seg_attn_tree_desc.from_buffer_copy(tab.desc)
+    bad.version = 99
+    assert h(A, A, A, A, A, A, ctypes.byref(bad), 0.1, A, ws, None) == I
+    empty = build([0], [[(0, 5)]])
+    assert h(None, None, None, None, None, None, ctypes.byref(empty.desc), 0.1, None, 0, None) == 0
+
+
+def test_binding_checks_dtypes_shapes_and_devices():
+    """The Python calls refuse CPU tensors (and say what they want)."""
+    x = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    pos = torch.zeros(2, dtype=torch.int32)
+    rope = sa.seg_attn_rope_plan(64)
+    pool = torch.zeros(8, 4, 128, dtype=torch.bfloat16)
+    assert code_of(lambda: sa.seg_attn_rope(x, x, pos, rope)) == S["INVALID_ARG"]
+    assert code_of(lambda: sa.seg_attn_rope_append(x, x, x, x, pos, pos, rope, pool, pool)) == \
+        S["INVALID_ARG"]
+    assert code_of(lambda: sa.seg_attn_kv_move(pool, pool, pos, pos)) == S["INVALID_ARG"]
+    tab = build([2], [[(0, 5)]], num_slots=8, hq=4, hkv=4)
+    assert code_of(lambda: sa.seg_attn_tree(x, pool, pool, x, None, tab.host, tab.desc, 0.1)) == \
+        S["INVALID_ARG"]
