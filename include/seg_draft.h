@@ -164,14 +164,12 @@ int seg_attn_rope_append_fp8(const void* q, int64_t q_stride, void* q_out, int64
 typedef struct seg_attn_tree_desc {
   uint32_t magic, version;
   int32_t batch, max_draft;
-  int64_t off_row;        /* [total_q][8] first drafted token of the request (packed), words
-                             of a mask row, first mask word (int32 offset in the table, low
-                             and high half), first prior item (-1: no cached keys), query row
-                             of kv head 0 in that item, two zeros */
-  int64_t off_mask;       /* mask words: bit j of word w of row i: i sees 32 w + j */
+  int64_t off_mask;       /* mask rows, requests back to back: ceil(draft_len / 32) words
+                             each, bit j of word w of row i: i sees drafted token 32 w + j */
   int64_t off_draft_slot; /* [total_q] pool slot of each drafted token */
-  int64_t off_citem;      /* [items][4] first partial slot, pieces, first query, 0 */
-  seg_attn_table_desc pass; /* the pass over the cached keys (offsets into the same buffer) */
+  seg_attn_table_desc pass; /* the prefill table of all keys (offsets into the same buffer);
+                               words 13, 14 of a work row: first mask word of the request
+                               (low and high half) */
   uint64_t table_bytes, workspace_bytes;
 } seg_attn_tree_desc;
 

@@ -108,8 +108,7 @@ class seg_attn_tree_desc(ctypes.Structure):
     _fields_ = [
         ("magic", ctypes.c_uint32), ("version", ctypes.c_uint32),
         ("batch", ctypes.c_int32), ("max_draft", ctypes.c_int32),
-        ("off_row", ctypes.c_int64), ("off_mask", ctypes.c_int64),
-        ("off_draft_slot", ctypes.c_int64), ("off_citem", ctypes.c_int64),
+        ("off_mask", ctypes.c_int64), ("off_draft_slot", ctypes.c_int64),
         ("pass_", seg_attn_table_desc),
         ("table_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64),
     ]

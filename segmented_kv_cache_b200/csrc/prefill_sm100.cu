@@ -16,7 +16,7 @@
 // loaded as two tiled boxes, which the TMA engine moves far faster than 64
 // four-row gathers.
 //
-// Warp roles (10 warps; 12 over an FP8 cache, see below):
+// Warp roles (two query tiles: 10 warps, 12 over an FP8 cache; one: 6 and 10):
 //   warp 0       TMA producer: Q tiles once, then a K ring and a V ring
 //                (stages per variant below), K tile i + 1 before V tile i.
 //   warp 1       TMEM allocator and MMA issuer: the whole warp runs the issue
@@ -42,9 +42,10 @@
 // One query tile: S double-buffered, each buffer with a P region of its own, so
 // the QK that refills an S buffer never overwrites what the PV before it reads.
 // TMEM columns: O [0,128) P0 [128,192) P1 [192,256) S0 [256,384) S1 [384,512).
-// Over an FP8 cache two more warps widen the E4M3 codes to f16: with two query
-// tiles in place, inside the ring slot whose second half the codes were loaded
-// into; with one, from staging tiles of their own.
+// Over an FP8 cache more warps (two; four with one query tile) widen the E4M3 codes
+// to f16 in place, inside the ring slot whose second half the codes were loaded into.
+// (A single staging tile per K and V, as the one-tile kernel had, exposed every tile's
+// load latency: 64 trees of 16 over 4k keys, 308 us against 87 us of cache reads.)
 // Every mbarrier wait is bounded (1 s); a timeout stops all roles of the CTA,
 // drains in-flight copies and MMAs, frees TMEM and flags a device error.
 #include <cuda.h>
@@ -66,10 +67,22 @@ __device__ int g_device_error;  // non-zero once a bounded wait gave up
 
 namespace {
 
-constexpr int kThreads = 320;
-// FP8 cache: two more warps (10, 11) widen E4M3 code tiles to f16 in shared memory
-constexpr int kThreadsFp8 = 384;
-constexpr int kConvThreads = 64;
+// Warps: producer, MMA issuer, four softmax warps per query tile, and over an FP8 cache
+// the warps that widen E4M3 codes (two with two query tiles, four with one, whose K
+// tiles come twice as fast).  Registers are dealt out per SM sub-partition: 6 warps
+// leave the one-tile bf16 kernel 255 per thread (no spills), 9 to 12 warps 168.
+template <bool SINGLE>
+constexpr int conv_warp0() {
+  return SINGLE ? 6 : 10;
+}
+template <bool SINGLE>
+constexpr int conv_threads() {
+  return SINGLE ? 128 : 64;
+}
+template <bool SINGLE, bool FP8>
+constexpr int cta_threads() {
+  return conv_warp0<SINGLE>() * 32 + (FP8 ? conv_threads<SINGLE>() : 0);
+}
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // default limit of a bounded wait
 // Stall test (off by default): the K tile at which every later prefill CTA's
 // producer stops loading (-1: none), and the limit of its bounded waits.
@@ -95,62 +108,37 @@ struct PrefillParams {
   uint64_t wait_ns;      // limit of every bounded wait (1 s unless a stall test shortens it)
   int withhold_tile;     // stall test: the producer stops before loading this K tile (-1: off)
   int p_delay_ns;        // order test: one-tile softmax sleep after the last P is signalled (0: off)
+  const uint32_t* mask_base;   // drafted tokens: the table, whose words hold the mask rows
+  const int32_t* draft_slot;   // drafted tokens: [total_q] pool slot of each
+  const void* v_pool;          // drafted tokens: V rows by address (the rare path of add_nonfinite)
 };
 
-// Query region + K ring + V ring + barriers + alignment slack.  The query
-// region is one Q tile (SINGLE) or the two P tiles, which hold the two Q tiles
-// until the softmax threads have moved them to tensor memory.  The d = 64
-// variant asks for more than half the SM's shared memory as well, so one CTA
-// owns an SM and its 512 tensor-memory columns.
-// K/V ring depths (stages of K, of V).  Over a bf16 cache the one-tile kernel
-// spends the second query tile's space on a third K and V stage; the two-tile
-// kernels, whose P tiles live in tensor memory, have room for a third K stage:
-// their QK of a K tile runs a softmax ahead of the PV of the previous one, so K
-// tiles are wanted earlier than V tiles.  The one-tile kernel over an FP8 cache
-// keeps two of each beside its code staging tiles.
-template <bool SINGLE, bool FP8>
-constexpr int ring_k() {
-  return SINGLE && FP8 ? 2 : 3;
-}
-template <bool SINGLE, bool FP8>
+// Query region (one Q tile or two) + K ring + V ring + barriers + alignment slack.
+// The d = 64 variant asks for more than half the SM's shared memory as well, so one
+// CTA owns an SM and its 512 tensor-memory columns.
+// K/V ring depths (stages of K, of V).  The one-tile kernel spends the second query
+// tile's space on a third V stage; the two-tile kernels' QK of a K tile runs a softmax
+// ahead of the PV of the previous one, so K tiles are wanted earlier than V tiles.
+constexpr int kRingK = 3;
+template <bool SINGLE>
 constexpr int ring_v() {
-  return SINGLE && !FP8 ? 3 : 2;
+  return SINGLE ? 3 : 2;
 }
 
-// Two query tiles: P in tensor memory columns of its own (so no MMA ever writes
-// tensor memory that an earlier MMA reads), one S buffer the two tiles take
-// turns on.  One query tile: S double-buffered, a P region per S buffer.  Queries
-// stay in shared memory as the TMA loaded them in both.
-template <bool SINGLE, bool FP8>
-constexpr bool two_tiles() {
-  return !SINGLE;
-}
+// An FP8 cache's E4M3 codes of a K/V tile land in the second half of its ring slot and
+// are widened to f16 there, so as many tiles are in flight as over a bf16 cache.
+constexpr size_t kBarrierBytes = 512;  // mbarriers, tensor-memory address, flags
 
-// FP8 cache, two query tiles: a K/V tile's E4M3 codes land in the second half of
-// its ring slot and are widened to f16 there (no staging tiles, which leaves the
-// shared memory the tensor-memory query layout needs).  One query tile: codes
-// are staged in tiles of their own and widened into the ring.
-template <bool SINGLE, bool FP8>
-constexpr bool widen_in_place() {
-  return FP8 && !SINGLE;
-}
-template <int D, bool SINGLE, bool FP8>
-constexpr size_t staging_bytes() {
-  return FP8 && !widen_in_place<SINGLE, FP8>() ? 2 * (size_t)kTileKeys * D : 0;
-}
-
-template <int D, bool SINGLE, bool FP8>
+template <int D, bool SINGLE>
 constexpr size_t query_region_bytes() {
   return (SINGLE ? 1 : 2) * (D / 64) * (size_t)kHalfBytes;
 }
 
-// The one-tile FP8 variant adds one staging tile of raw codes each for K and V.
-template <int D, bool SINGLE, bool FP8>
+template <int D, bool SINGLE>
 constexpr size_t prefill_smem_bytes() {
-  constexpr size_t need = query_region_bytes<D, SINGLE, FP8>() +
-                          (ring_k<SINGLE, FP8>() + ring_v<SINGLE, FP8>()) * (D / 64) *
-                              (size_t)kHalfBytes +
-                          staging_bytes<D, SINGLE, FP8>() + 256 + 1024;
+  constexpr size_t need = query_region_bytes<D, SINGLE>() +
+                          (kRingK + ring_v<SINGLE>()) * (D / 64) * (size_t)kHalfBytes +
+                          kBarrierBytes + 1024;
   static_assert(need <= 227 * 1024, "shared memory per CTA");
   return need < 120 * 1024 ? 120 * 1024 : need;
 }
@@ -197,49 +185,20 @@ __device__ __forceinline__ void bf16x8_to_f16x8(uint4& v) {
     w[i] = ptx::pack_f16x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-// One tile of E4M3 codes (kTileKeys rows of D bytes, plain row-major) -> f16
-// in the 128-byte-swizzled K-major layout the tensor cores read (the layout a
-// tiled TMA load of a bf16 tile produces): row r, 16-byte chunk c of 64-column
-// half h lands at h * kHalfBytes + r * 128 + ((c ^ (r & 7)) * 16).  Thread ct
-// owns one 16-code column j of rows r0, r0 + step, ... with step a multiple of
-// 8, so the swizzle phase r & 7 and both store offsets are fixed per thread and
-// the unrolled loop needs no address arithmetic.
-template <int D>
-__device__ __forceinline__ void widen_tile(const uint8_t* src, uint8_t* dst, int ct) {
-  constexpr int kCols = D / 16;                   // 16-code units per row
-  constexpr int kRowStep = kConvThreads / kCols;  // 8 (d = 128) or 16 (d = 64)
-  static_assert(kRowStep % 8 == 0, "rows of one thread must share the swizzle phase");
-  const int j = ct % kCols, r0 = ct / kCols;
-  const int sw = r0 & 7, c0 = (j & 3) * 2;
-  const uint8_t* s = src + r0 * D + 16 * j;
-  uint8_t* d = dst + (j >> 2) * kHalfBytes + r0 * 128;
-  const int o0 = (c0 ^ sw) << 4, o1 = ((c0 + 1) ^ sw) << 4;
-#pragma unroll
-  for (int k = 0; k < kTileKeys / kRowStep; ++k) {
-    const uint4 w = *reinterpret_cast<const uint4*>(s + k * kRowStep * D);
-    uint4 lo, hi;
-    lo.x = ptx::e4m3x2_to_f16x2(w.x);
-    lo.y = ptx::e4m3x2_to_f16x2(w.x >> 16);
-    lo.z = ptx::e4m3x2_to_f16x2(w.y);
-    lo.w = ptx::e4m3x2_to_f16x2(w.y >> 16);
-    hi.x = ptx::e4m3x2_to_f16x2(w.z);
-    hi.y = ptx::e4m3x2_to_f16x2(w.z >> 16);
-    hi.z = ptx::e4m3x2_to_f16x2(w.w);
-    hi.w = ptx::e4m3x2_to_f16x2(w.w >> 16);
-    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o0) = lo;
-    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o1) = hi;
-  }
-}
-
-// In-place variant: the codes of one tile sit in the second half of the ring slot
-// (rows of D bytes) and are widened into the whole slot, in the layout above.  A
-// row's f16 output overwrites code bytes that other threads read, so every thread
-// first loads all of its codes, the 64 widening threads meet at named barrier 1,
+// The E4M3 codes of one tile, in the second half of a ring slot (kTileKeys rows of D
+// bytes, plain row-major) -> f16 over the whole slot in the 128-byte-swizzled K-major
+// layout the tensor cores read (the layout a tiled TMA load of a bf16 tile produces):
+// row r, 16-byte chunk c of 64-column half h lands at h * kHalfBytes + r * 128 +
+// ((c ^ (r & 7)) * 16).  Thread ct of the NT widening threads owns one 16-code column j
+// of rows r0, r0 + step, ... with step a multiple of 8, so the swizzle phase r & 7 and
+// both store offsets are fixed per thread and the unrolled loop needs no address
+// arithmetic.  A row's f16 output overwrites code bytes that other threads read, so
+// every thread first loads all of its codes, the NT threads meet at named barrier 1,
 // and only then write.
-template <int D>
+template <int D, int NT>
 __device__ __forceinline__ void widen_tile_in_place(uint8_t* slot, int ct) {
   constexpr int kCols = D / 16;
-  constexpr int kRowStep = kConvThreads / kCols;
+  constexpr int kRowStep = NT / kCols;
   constexpr int kRows = kTileKeys / kRowStep;
   static_assert(kRowStep % 8 == 0, "rows of one thread must share the swizzle phase");
   const int j = ct % kCols, r0 = ct / kCols;
@@ -247,7 +206,7 @@ __device__ __forceinline__ void widen_tile_in_place(uint8_t* slot, int ct) {
   uint4 w[kRows];
 #pragma unroll
   for (int k = 0; k < kRows; ++k) w[k] = *reinterpret_cast<const uint4*>(s + k * kRowStep * D);
-  ptx::named_barrier(1, kConvThreads);
+  ptx::named_barrier(1, NT);
   const int sw = r0 & 7, c0 = (j & 3) * 2;
   uint8_t* d = slot + (j >> 2) * kHalfBytes + r0 * 128;
   const int o0 = (c0 ^ sw) << 4, o1 = ((c0 + 1) ^ sw) << 4;
@@ -271,12 +230,18 @@ __device__ __forceinline__ void widen_tile_in_place(uint8_t* slot, int ct) {
 // (the planner lists those items last and launches them separately, so each
 // instantiation keeps its own register allocation).
 // FP8: the pools hold E4M3 codes (value = code * scale of the kv head).  Code
-// tiles are staged by TMA as raw bytes and widened to f16 (exact) by warps 10
-// and 11 into the K/V rings; queries are converted bf16 -> f16 in shared memory
+// tiles are loaded by TMA as raw bytes and widened to f16 (exact) in the K/V ring
+// slots by the last warps; queries are converted bf16 -> f16 in shared memory
 // and P is f16, so every product is f16 x f16 -> f32.  The K scale is folded
 // into the softmax scale, the V scale into the output.
-template <int D, bool SINGLE, bool FP8, bool TMA_OUT>
-__global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
+// TREE: the last q_len keys of a request are its drafted tokens, the queries of this
+// call; a query sees every key before them and those its mask row has bits for.  Only
+// the K tiles that reach past the cached keys look at the mask.  P of a masked key is
+// an exact zero, but zero times an infinite or NaN value would still reach the row in
+// P.V, so in those tiles non-finite values of drafted keys are replaced by zeros in the
+// V tile, and the rows that do see such a key get them added at the end.
+template <int D, bool SINGLE, bool FP8, bool TMA_OUT, bool TREE>
+__global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k3,
                    const __grid_constant__ CUtensorMap tm_v3, const __grid_constant__ CUtensorMap tm_o,
@@ -288,18 +253,16 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
-  constexpr int RK = ring_k<SINGLE, FP8>(), RV = ring_v<SINGLE, FP8>();
+  constexpr int RK = kRingK, RV = ring_v<SINGLE>();
+  constexpr int kConvWarp0 = conv_warp0<SINGLE>(), kConvThreads = conv_threads<SINGLE>();
   // Q tiles at sQ + t * TILE.  Two query tiles (QT): P_t in tensor memory columns
   // [384 + 64 t, 448 + 64 t).
-  constexpr bool QT = two_tiles<SINGLE, FP8>();
+  constexpr bool QT = !SINGLE;
   constexpr uint32_t QSTRIDE = TILE;
   uint8_t* sQ = sm;
-  uint8_t* sK = sm + query_region_bytes<D, SINGLE, FP8>();
+  uint8_t* sK = sm + query_region_bytes<D, SINGLE>();
   uint8_t* sV = sK + RK * TILE;
-  constexpr bool INPLACE = widen_in_place<SINGLE, FP8>();
-  uint8_t* sStK = sV + RV * TILE;           // FP8, one tile: raw code tile of K
-  uint8_t* sStV = sStK + kTileKeys * D;     // FP8, one tile: raw code tile of V
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + RV * TILE + staging_bytes<D, SINGLE, FP8>());
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + RV * TILE);
   uint64_t* q_full = bars + 0;
   uint64_t* k_full = bars + 1;    // [RK]
   uint64_t* k_empty = bars + 4;   // [RK]
@@ -309,16 +272,13 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
   uint64_t* p_full = bars + 15;   // [2]
   uint64_t* o_full = bars + 17;   // [2]
   uint64_t* mma_done = bars + 19;
-  uint64_t* kst_full = bars + 20;   // FP8, one tile: code staging of K filled (TMA bytes)
-  uint64_t* kst_empty = bars + 21;  // FP8, one tile: code staging of K read by the converters
-  uint64_t* vst_full = bars + 22;
-  uint64_t* vst_empty = bars + 23;
-  uint64_t* code_k = bars + 20;     // FP8 in place: [RK] codes landed in a K ring slot
-  uint64_t* code_v = bars + 30;     // FP8 in place: [RV] the same for V
+  uint64_t* code_k = bars + 20;     // FP8: [RK] codes landed in a K ring slot
+  uint64_t* code_v = bars + 30;     // FP8: [RV] the same for V
   uint64_t* q_conv = bars + 24;     // FP8: queries converted to f16 in place
   uint64_t* s_free = bars + 25;     // two tiles: the shared S buffer read by its softmax
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* nonfinite = reinterpret_cast<int*>(bars + 34);  // TREE: some drafted V value was not finite
   // limit of every bounded wait, read only when a wait checks it
   volatile uint64_t* wait_limit = reinterpret_cast<volatile uint64_t*>(bars + 29);
 
@@ -358,16 +318,12 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     mbar_init(mma_done, 1);
     mbar_init(s_free, 4);  // one arrival per softmax warp of the tile that read S
     mbar_init(q_conv, (SINGLE ? 1 : 2) * 128);
-    if (INPLACE) {
+    if (FP8) {
       for (int s = 0; s < RK; ++s) mbar_init(code_k + s, 1);
       for (int s = 0; s < RV; ++s) mbar_init(code_v + s, 1);
-    } else if (FP8) {
-      mbar_init(kst_full, 1);
-      mbar_init(kst_empty, kConvThreads);
-      mbar_init(vst_full, 1);
-      mbar_init(vst_empty, kConvThreads);
     }
     *abort_flag = 0;
+    *nonfinite = 0;
     *wait_limit = p.wait_ns;
     fence_mbar_init();
   }
@@ -461,7 +417,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
                         tr.rows[1], tr.rows[2], tr.rows[3]);
         }
       };
-      // FP8: raw code rows (D bytes each) into the staging tile, no swizzle
+      // FP8: raw code rows (D bytes each), no swizzle
       auto load_codes = [&](const TileRows& tr, uint8_t* dst, const CUtensorMap* tiled,
                             const CUtensorMap* rowmap, uint64_t* bar) {
         if (lane == 0) mbar_expect_tx(bar, kTileKeys * D);
@@ -481,7 +437,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         if (!__all_sync(0xffffffffu, mbar_wait(k_empty + st, ((i / RK) & 1) ^ 1, abort_flag,
                                                wait_limit, true)))
           return false;
-        if (INPLACE)  // codes into the slot's second half, widened there by warps 10-11
+        if (FP8)  // codes into the slot's second half, widened there by the last warps
           load_codes(tr, sK + st * TILE + TILE / 2, &tm_k3, &tm_k, code_k + st);
         else
           load_tile(tr, sK + st * TILE, &tm_k3, &tm_k, k_full + st);
@@ -493,57 +449,38 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         if (!__all_sync(0xffffffffu, mbar_wait(v_empty + st, ((i / RV) & 1) ^ 1, abort_flag,
                                                wait_limit, true)))
           return false;
-        if (INPLACE)
+        if (FP8)
           load_codes(tr, sV + st * TILE + TILE / 2, &tm_v3, &tm_v, code_v + st);
         else
           load_tile(tr, sV + st * TILE, &tm_v3, &tm_v, v_full + st);
         ++v_issued;
         return true;
       };
-      if (FP8 && !INPLACE) {
-        // codes of K tile i, then of V tile i, through one staging tile each
-        for (int i = 0; i < n_tiles; ++i) {
-          TileRows tr;
-          tile_rows(i, tr);
-          if (i == p.withhold_tile) break;  // stall test (see load_k)
-          if (!__all_sync(0xffffffffu, mbar_wait(kst_empty, (i & 1) ^ 1, abort_flag, wait_limit, true))) break;
-          load_codes(tr, sStK, &tm_k3, &tm_k, kst_full);
-          ++k_issued;
-          if (!__all_sync(0xffffffffu, mbar_wait(vst_empty, (i & 1) ^ 1, abort_flag, wait_limit, true))) break;
-          load_codes(tr, sStV, &tm_v3, &tm_v, vst_full);
-          ++v_issued;
+      // K tile i + 1 before V tile i: the MMA warp takes them in that order
+      TileRows cur, nxt;
+      tile_rows(0, cur);
+      if (k0_early) ++k_issued;
+      bool run = k0_early || load_k(0, cur);
+      for (int i = 0; run && i < n_tiles; ++i) {
+        if (i + 1 < n_tiles) {
+          tile_rows(i + 1, nxt);
+          if (!(run = load_k(i + 1, nxt))) break;
         }
-        // never leave the CTA with copies in flight (a staged copy is issued only
-        // after the converters read the previous one, so the last is enough)
-        if (k_issued > 0) mbar_wait(kst_full, (k_issued - 1) & 1, nullptr, wait_limit);
-        if (v_issued > 0) mbar_wait(vst_full, (v_issued - 1) & 1, nullptr, wait_limit);
-      } else {
-        // K tile i + 1 before V tile i: the MMA warp takes them in that order
-        TileRows cur, nxt;
-        tile_rows(0, cur);
-        if (k0_early) ++k_issued;
-        bool run = k0_early || load_k(0, cur);
-        for (int i = 0; run && i < n_tiles; ++i) {
-          if (i + 1 < n_tiles) {
-            tile_rows(i + 1, nxt);
-            if (!(run = load_k(i + 1, nxt))) break;
-          }
-          if (!(run = load_v(i, cur))) break;
-          cur = nxt;
-        }
-        // never leave the CTA with copies in flight (the copies' own barriers: in
-        // place, the ring slots' full barriers wait for the widening threads too)
-        for (int s = 0; s < RK; ++s)
-          if (k_issued > s) {
-            const int last = s + RK * ((k_issued - 1 - s) / RK);
-            mbar_wait((INPLACE ? code_k : k_full) + s, (last / RK) & 1, nullptr, wait_limit);
-          }
-        for (int s = 0; s < RV; ++s)
-          if (v_issued > s) {
-            const int last = s + RV * ((v_issued - 1 - s) / RV);
-            mbar_wait((INPLACE ? code_v : v_full) + s, (last / RV) & 1, nullptr, wait_limit);
-          }
+        if (!(run = load_v(i, cur))) break;
+        cur = nxt;
       }
+      // never leave the CTA with copies in flight (the copies' own barriers:
+      // over an FP8 cache the slots' full barriers wait for the widening threads too)
+      for (int s = 0; s < RK; ++s)
+        if (k_issued > s) {
+          const int last = s + RK * ((k_issued - 1 - s) / RK);
+          mbar_wait((FP8 ? code_k : k_full) + s, (last / RK) & 1, nullptr, wait_limit);
+        }
+      for (int s = 0; s < RV; ++s)
+        if (v_issued > s) {
+          const int last = s + RV * ((v_issued - 1 - s) / RV);
+          mbar_wait((FP8 ? code_v : v_full) + s, (last / RV) & 1, nullptr, wait_limit);
+        }
       if (lane == 0) mbar_wait(q_full, 0, nullptr, wait_limit);
     }
   } else if (warp == 1) {
@@ -708,52 +645,33 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       mbar_wait(mma_done, 0, nullptr, wait_limit);
     }
     __syncwarp();
-  } else if (FP8 && warp >= 10) {
+  } else if (FP8 && warp >= kConvWarp0) {
     // ------------------------------------------------------------ FP8 code widening
     // E4M3 tile -> f16 K (V) ring slot, then make the generic-proxy writes
     // visible to the tensor cores before signalling the ring slot full.
-    const int ct = threadIdx.x - 10 * 32;
+    const int ct = threadIdx.x - kConvWarp0 * 32;
     bool ok = true;
-    if (INPLACE) {
-      // codes in the slot's second half, in the producer's order: K tile 0, then
-      // K tile i + 1 before V tile i.  The 64 threads agree on every wait's outcome
-      // at a barrier (all or none go on), since the widening meets at another one.
-      auto widen = [&](uint8_t* slot, uint64_t* landed, uint32_t parity, uint64_t* full) -> bool {
-        const bool got = mbar_wait(landed, parity, abort_flag, wait_limit);
-        if (!named_barrier_and(1, kConvThreads, got)) return false;
-        widen_tile_in_place<D>(slot, ct);
-        fence_proxy_async_smem();
-        mbar_arrive(full);
-        return true;
-      };
-      if (n_tiles > 0) ok = widen(sK, code_k, 0, k_full);
-      for (int i = 0; ok && i < n_tiles; ++i) {
-        if (i + 1 < n_tiles) {
-          const int sk = (i + 1) % RK;
-          if (!(ok = widen(sK + sk * TILE, code_k + sk, ((i + 1) / RK) & 1, k_full + sk))) break;
-        }
-        const int sv = i % RV;
-        ok = widen(sV + sv * TILE, code_v + sv, (i / RV) & 1, v_full + sv);
+    // codes in the slot's second half, in the producer's order: K tile 0, then K tile
+    // i + 1 before V tile i.  The widening threads agree on every wait's outcome at a
+    // barrier (all or none go on), since the widening meets at another one.
+    auto widen = [&](uint8_t* slot, uint64_t* landed, uint32_t parity, uint64_t* full) -> bool {
+      const bool got = mbar_wait(landed, parity, abort_flag, wait_limit);
+      if (!named_barrier_and(1, kConvThreads, got)) return false;
+      widen_tile_in_place<D, kConvThreads>(slot, ct);
+      fence_proxy_async_smem();
+      mbar_arrive(full);
+      return true;
+    };
+    if (n_tiles > 0) ok = widen(sK, code_k, 0, k_full);
+    for (int i = 0; ok && i < n_tiles; ++i) {
+      if (i + 1 < n_tiles) {
+        const int sk = (i + 1) % RK;
+        if (!(ok = widen(sK + sk * TILE, code_k + sk, ((i + 1) / RK) & 1, k_full + sk))) break;
       }
+      const int sv = i % RV;
+      ok = widen(sV + sv * TILE, code_v + sv, (i / RV) & 1, v_full + sv);
     }
-    for (int i = 0; !INPLACE && ok && i < n_tiles; ++i) {
-      const int sk = i % RK, sv = i % RV;
-      if (!(ok = mbar_wait(kst_full, i & 1, abort_flag, wait_limit) &&
-                 mbar_wait(k_empty + sk, ((i / RK) & 1) ^ 1, abort_flag, wait_limit)))
-        break;
-      widen_tile<D>(sStK, sK + sk * TILE, ct);
-      fence_proxy_async_smem();
-      mbar_arrive(k_full + sk);
-      mbar_arrive(kst_empty);
-      if (!(ok = mbar_wait(vst_full, i & 1, abort_flag, wait_limit) &&
-                 mbar_wait(v_empty + sv, ((i / RV) & 1) ^ 1, abort_flag, wait_limit)))
-        break;
-      widen_tile<D>(sStV, sV + sv * TILE, ct);
-      fence_proxy_async_smem();
-      mbar_arrive(v_full + sv);
-      mbar_arrive(vst_empty);
-    }
-  } else if (!single || warp < 6) {
+  } else {
     // ------------------------------------------------------------ softmax + epilogue
     const int t = (warp - 2) >> 2;
     const int quad = warp & 3;
@@ -761,7 +679,24 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     const int qi = q0 + t * p.qpt + row / p.group;
     const int head = g * p.group + row % p.group;
     const bool row_valid = qi < q_len;
-    const int vis = p.causal ? min(k_len, k_len - q_len + qi + 1) : k_len;
+    const int prior = k_len - q_len;  // TREE: keys before the drafted ones
+    const uint32_t* mask_row = nullptr;
+    if (TREE && row_valid)
+      mask_row = p.mask_base + ((uint64_t)(uint32_t)w3.y | ((uint64_t)(uint32_t)w3.z << 32)) +
+                 (int64_t)qi * ((q_len + 31) >> 5);
+    // TREE: which of the 32 keys from drafted key `at` on this row sees (at < 0: cached
+    // keys, all seen, come first)
+    auto mask_word = [&](int at) -> uint32_t {
+      if (at <= -32) return 0xffffffffu;
+      if (!mask_row) return 0u;
+      const int words = (q_len + 31) >> 5;
+      if (at < 0) return (__ldg(mask_row) << -at) | ((1u << -at) - 1u);
+      const int w = at >> 5;
+      const uint32_t lo = w < words ? __ldg(mask_row + w) : 0u;
+      const uint32_t hi = w + 1 < words ? __ldg(mask_row + w + 1) : 0u;
+      return __funnelshift_r(lo, hi, at & 31);
+    };
+    const int vis = TREE ? prior : p.causal ? min(k_len, k_len - q_len + qi + 1) : k_len;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     uint32_t tS = lane_base + 256 + 128 * t;  // S buffer of the current K tile (SINGLE)
     if (QT) tS = lane_base + 256;             // two tiles: the shared S buffer
@@ -773,6 +708,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     const float sl2 = FP8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
     float m_ref = -INFINITY;  // raw score units
     float l = 0.f;
+    // a row that saw a NaN score has a NaN sum, which its lse shows (drafted tokens)
+    auto has_keys = [](float sum) { return TREE ? sum != 0.f : sum > 0.f; };
     bool ok = true;
     if (n_tiles > 0 && FP8) {
       // FP8 cache: this thread's query row of tile t, bf16 -> f16 in place (exact
@@ -814,10 +751,14 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       if (masked) {
         const int kb = (kt0 + i) * kTileKeys;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t word = TREE ? mask_word(kb + 32 * c - prior) : 0u;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (kb + 32 * c + e >= vis) sv[c][e] = 0xff800000u;  // -inf
+          for (int e = 0; e < 32; ++e) {
+            const bool hide = TREE ? !((word >> e) & 1u) : kb + 32 * c + e >= vis;
+            if (hide) sv[c][e] = 0xff800000u;  // -inf
+          }
+        }
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -911,6 +852,39 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       return __all_sync(0xffffffffu,
                         mbar_wait(o_full + t, (i - 1) & 1, abort_flag, wait_limit)) != 0;
     };
+    // TREE, tile with drafted keys: V row `row` of the tile, when it is a drafted key's (or
+    // past the last key), gets zeros for values that are not finite.  Query tile 0's
+    // threads do it before they signal P; the PV of tile 1 is issued after tile 0's.
+    auto clean_v = [&](int i) -> bool {
+      const int sv = i % RV;
+      if (!__all_sync(0xffffffffu, mbar_wait(v_full + sv, (i / RV) & 1, abort_flag, wait_limit)))
+        return false;
+      if ((kt0 + i) * kTileKeys + row < prior) return true;
+      constexpr uint32_t kExp = FP8 ? 0x7c00u : 0x7f80u;  // f16 (widened) or bf16
+      bool found = false;
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(sV + sv * TILE + h * kHalfBytes + row * 128 +
+                                                    ((c ^ (row & 7)) << 4));
+          const uint4 v = *reinterpret_cast<const uint4*>(w);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool lo = (x[e] & kExp) == kExp, hi = (x[e] & (kExp << 16)) == (kExp << 16);
+            if (lo || hi) {
+              w[e] = (lo ? 0u : x[e] & 0xffffu) | (hi ? 0u : x[e] & 0xffff0000u);
+              found = true;
+            }
+          }
+        }
+      if (found) {
+        *reinterpret_cast<volatile int*>(nonfinite) = 1;
+        fence_proxy_async_smem();
+      }
+      return true;
+    };
     // one K tile of softmax on S buffer sb (phase sph of its barriers)
     auto run_tile = [&](int i, int sb, uint32_t sph) -> bool {
       if (single) {
@@ -930,6 +904,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
             return false;
         }
         if (!last_pv_order(i)) return false;
+        if (TREE && t == 0 && (kt0 + i + 1) * kTileKeys > prior && !clean_v(i)) return false;
         mbar_arrive(p_full + sb);
         return true;
       }
@@ -938,6 +913,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       if (!softmax_tile(i, masked)) return false;
       tmem_wait_st();
       if (!last_pv_order(i)) return false;
+      if (TREE && t == 0 && masked && !clean_v(i)) return false;
       tc_fence_before();
       mbar_arrive(p_full + sb);
       return true;
@@ -958,10 +934,43 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       if (p.p_delay_ns > 0 && ok) __nanosleep(p.p_delay_ns);
     }
     if (!warp_live) ok = false;  // nothing to write
+    // TREE, after some drafted V value was not finite: what this row sees of them is added
+    // to O in tensor memory, as its product with a positive weight would be (a NaN or an
+    // infinity).  32 columns at a time, every lane of the warp in step.
+    auto add_nonfinite = [&]() {
+      const int first = max(kt0 * kTileKeys - prior, 0);
+      const int last = min((kt0 + n_tiles) * kTileKeys - prior, q_len);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * c, o);
+        tmem_wait_ld(o);
+#pragma unroll 1
+        for (int j = first; j < last; ++j) {
+          const bool seen = mask_word(j) & 1u;
+          const int64_t at =
+              ((int64_t)__ldg(p.draft_slot + tok0 + j) * p.kv_heads + g) * D + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x = 0.f;
+            if (FP8) {
+              if ((static_cast<const uint8_t*>(p.v_pool)[at + e] & 0x7f) == 0x7f) x = NAN;
+            } else {
+              const uint32_t b = static_cast<const uint16_t*>(p.v_pool)[at + e];
+              if ((b & 0x7f80) == 0x7f80) x = __uint_as_float(b << 16);
+            }
+            if (seen && x != 0.f) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+          }
+        }
+        tmem_st32(tO + 32 * c, o);
+      }
+      tmem_wait_st();
+    };
     // this row's O (fp32, D columns) in registers: every load issued, one wait
     auto load_o = [&](uint32_t (&o)[D / 32][32]) {
       if (n_tiles > 0) {
         tc_fence_after();
+        if (TREE && *reinterpret_cast<volatile int*>(nonfinite) != 0) add_nonfinite();
         if constexpr (D == 128) {
           tmem_ld128(tO, o);
         } else {
@@ -999,7 +1008,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       constexpr int PCOLS = (int)(QSTRIDE / 512) < D ? (int)(QSTRIDE / 512) : D;
       constexpr int PCH = PCOLS / 4;        // 16-byte chunks per row per pass
       constexpr int RPI = 32 / PCH;         // rows per warp instruction of the copy
-      const float inv = l > 0.f ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
+      const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
       const int64_t prow0 = (int64_t)slot * kItemRows + t * kTileRows + quad * 32;
       uint32_t o[D / 32][32];
       load_o(o);
@@ -1025,12 +1034,12 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         }
         __syncwarp();
       }
-      if (row_valid) p.part_lse[prow0 + lane] = l > 0.f ? m_ref * sl2 + log2f(l) : -INFINITY;
+      if (row_valid) p.part_lse[prow0 + lane] = has_keys(l) ? m_ref * sl2 + log2f(l) : -INFINITY;
     } else if (!TMA_OUT && ok) {
       // a pass whose pieces mostly write partials: rows staged per warp, copied out
       constexpr int CH = D / 8;    // 16-byte chunks of a bf16 row
       constexpr int RPI = 32 / CH; // rows per warp instruction of the copy
-      const float inv = l > 0.f ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
+      const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
       uint32_t o[D / 32][32];
       load_o(o);
 #pragma unroll
@@ -1058,7 +1067,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       }
       if (row_valid && p.lse)
         p.lse[(int64_t)(tok0 + qi) * p.q_heads + head] =
-            l > 0.f ? (m_ref * sl2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            has_keys(l) ? (m_ref * sl2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
     if (TMA_OUT && slot < 0) {
       // Final bf16 output, staged in the tile's query region in the layout of the
@@ -1075,7 +1084,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       const bool full = q0 + (t + 1) * p.qpt <= q_len;
       const bool go = full ? named_barrier_and(2 + t, 128, ok) : ok;
       if (go) {
-        const float inv = l > 0.f ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
+        const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
         uint32_t o[D / 32][32];
         load_o(o);
 #pragma unroll
@@ -1118,7 +1127,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         }
         if (row_valid && p.lse)
           p.lse[(int64_t)(tok0 + qi) * p.q_heads + head] =
-              l > 0.f ? (m_ref * sl2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+              has_keys(l) ? (m_ref * sl2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
     }
   }
@@ -1204,21 +1213,21 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool SINGLE, bool FP8, bool TMA_OUT>
+template <int D, bool SINGLE, bool FP8, bool TMA_OUT, bool TREE>
 int launch_items(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                  const CUtensorMap& tk3, const CUtensorMap& tv3, const CUtensorMap& to,
                  const PrefillParams& p, int n,
                  cudaStream_t stream) {
-  constexpr size_t smem = prefill_smem_bytes<D, SINGLE, FP8>();
-  if (cudaFuncSetAttribute(prefill_kernel<D, SINGLE, FP8, TMA_OUT>,
+  constexpr size_t smem = prefill_smem_bytes<D, SINGLE>();
+  if (cudaFuncSetAttribute(prefill_kernel<D, SINGLE, FP8, TMA_OUT, TREE>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SEG_ATTN_ERR_CUDA;
-  prefill_kernel<D, SINGLE, FP8, TMA_OUT><<<n, FP8 ? kThreadsFp8 : kThreads, smem, stream>>>(tq, tk, tv, tk3,
-                                                                                  tv3, to, p);
+  prefill_kernel<D, SINGLE, FP8, TMA_OUT, TREE>
+      <<<n, cta_threads<SINGLE, FP8>(), smem, stream>>>(tq, tk, tv, tk3, tv3, to, p);
   return cudaGetLastError() == cudaSuccess ? SEG_ATTN_OK : SEG_ATTN_ERR_CUDA;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool TREE>
 int launch_prefill_d(const PrefillLaunch& a, cudaStream_t stream) {
   const seg_attn_table_desc& d = *a.desc;
   const int group = d.q_heads / d.kv_heads;
@@ -1271,15 +1280,19 @@ int launch_prefill_d(const PrefillLaunch& a, cudaStream_t stream) {
   p.wait_ns = g_stall_wait_ns.load();
   p.withhold_tile = g_stall_tile.load();
   p.p_delay_ns = g_order_delay_ns.load();
+  p.mask_base = a.mask_base;
+  p.draft_slot = a.draft_slot;
+  p.v_pool = a.v_pool;
   // two-tile items first, then the single-tile items listed at the end.  A pass in
   // which some piece writes final rows runs the instantiation whose epilogue stores
   // full query tiles by TMA; a pass of partials only (every item split, or a pass
   // over shared prefixes) keeps the leaner epilogue, which measured faster there.
   const int n_single = d.num_single, n_two = d.num_work - d.num_single;
-  const bool any_final = d.num_parts < d.num_work;
+  // Drafted tokens always run the former: their passes are mostly unsplit.
+  const bool any_final = TREE || d.num_parts < d.num_work;
   auto launch = [&](auto single_tag, auto tma_tag, int base, int n) {
     p.work_base = base;
-    return launch_items<D, decltype(single_tag)::value, FP8, decltype(tma_tag)::value>(
+    return launch_items<D, decltype(single_tag)::value, FP8, decltype(tma_tag)::value || TREE, TREE>(
         tq, tk, tv, tk3, tv3, to, p, n, stream);
   };
   using T = std::true_type;
@@ -1292,7 +1305,7 @@ int launch_prefill_d(const PrefillLaunch& a, cudaStream_t stream) {
     const int rc = any_final ? launch(T{}, T{}, n_two, n_single) : launch(T{}, F{}, n_two, n_single);
     if (rc != SEG_ATTN_OK) return rc;
   }
-  if (d.num_merge > 0) {
+  if (!TREE && d.num_merge > 0) {
     prefill_merge_kernel<D><<<dim3(d.num_merge, 4), 256, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SEG_ATTN_ERR_CUDA;
   }
@@ -1302,11 +1315,15 @@ int launch_prefill_d(const PrefillLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 int launch_prefill(const PrefillLaunch& a, cudaStream_t stream) {
-  if (a.fp8)
-    return a.desc->head_dim == 128 ? launch_prefill_d<128, true>(a, stream)
-                                   : launch_prefill_d<64, true>(a, stream);
-  return a.desc->head_dim == 128 ? launch_prefill_d<128, false>(a, stream)
-                                 : launch_prefill_d<64, false>(a, stream);
+  auto launch = [&](auto fp8_tag, auto tree_tag) {
+    constexpr bool F = decltype(fp8_tag)::value, T = decltype(tree_tag)::value;
+    return a.desc->head_dim == 128 ? launch_prefill_d<128, F, T>(a, stream)
+                                   : launch_prefill_d<64, F, T>(a, stream);
+  };
+  std::true_type yes;
+  std::false_type no;
+  if (a.mask_base) return a.fp8 ? launch(yes, yes) : launch(no, yes);
+  return a.fp8 ? launch(yes, no) : launch(no, no);
 }
 
 namespace {

@@ -17,6 +17,7 @@ constexpr int kMinPieceTiles = 8;       // shortest K range a split prefill piec
 constexpr int kPieceOverheadTiles = 3;  // per-piece cost (prologue, epilogue) in K tiles (traced: ~12 k cycles)
 constexpr int kMaxSplit = 4;            // most pieces one prefill item is cut into
 constexpr int kMaxGroupSplit = 32;      // the same for a pass over a shared prefix
+constexpr int kTreeMinPieceTiles = 2;   // the shortest K range of a piece of drafted tokens
 constexpr int kMinSharedKeys = 256;     // shortest prefix worth a pass of its own
 // decode: key chunks are halved (down to 256 keys) until the grid has this many
 // CTAs -- 4 waves at 2 CTAs per SM, so the last wave's tail stays short
@@ -91,6 +92,10 @@ struct PrefillLaunch {
   bool fp8 = false;                // pools hold E4M3 codes
   const float* k_scale = nullptr;  // [Hkv] device, FP8 only
   const float* v_scale = nullptr;
+  // drafted tokens (tree table): the table as words and the drafted tokens' slots; the
+  // caller merges split items itself
+  const uint32_t* mask_base = nullptr;
+  const int32_t* draft_slot = nullptr;
 };
 
 struct DecodeLaunch {

@@ -1,9 +1,9 @@
 // Host side of the drafted-token attention: validator, mask words and work plan.
 //
-// The pass over the cached keys is the prefill kernel run without a causal mask
-// on each request's first P keys, every piece writing a partial, exactly as the
-// pass over shared prefixes is; the drafted tokens' own keys, of which a token
-// sees a handful, are left to the kernel that joins the partials (tree.cu).
+// The table is that of a prefill without a causal mask, whose work rows also say
+// where the request's mask rows begin; the K tiles that reach past the cached keys
+// look at them.  Few items are cut finely along the keys (down to
+// kTreeMinPieceTiles tiles a piece), so that one request's call fills the SMs too.
 #include <stdint.h>
 #include <string.h>
 
@@ -42,7 +42,7 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   if (nseg_in > kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
   if (nseg_in > 0 && (!seg_starts || !seg_lens)) return SEG_ATTN_ERR_INVALID_ARG;
 
-  std::vector<int32_t> q_off(batch + 1, 0), prior(batch), draft_slot;
+  std::vector<int32_t> q_off(batch + 1, 0), keys(batch), draft_slot;
   std::vector<Segs> own(batch);
   std::vector<uint32_t> words;            // mask words, rows back to back
   std::vector<int64_t> mask_at(batch);    // first word of each request
@@ -72,8 +72,8 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
     if (t < 0) return SEG_ATTN_ERR_INVALID_ARG;
     if (t > SEG_ATTN_TREE_MAX_DRAFT) return SEG_ATTN_ERR_UNSUPPORTED;
     if (t > k) return SEG_ATTN_ERR_QLEN_GT_KLEN;
-    prior[r] = (int32_t)(k - t);
-    own[r] = cut(all, 0, k - t);
+    keys[r] = (int32_t)k;
+    own[r] = cut(all, 0, k);  // without empty segments
     nseg += (int64_t)own[r].len.size();
     const Segs drafts = cut(all, k - t, t);
     for (size_t i = 0; i < drafts.len.size(); ++i)
@@ -99,34 +99,30 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
     }
     mask0 += (int64_t)t * t;
     total_q += t;
-    total_k += prior[r];
+    total_k += k;
     if (total_q > kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
     q_off[r + 1] = (int32_t)total_q;
     max_draft = std::max(max_draft, t);
   }
 
-  // ---- the pass over the cached keys
+  // ---- work plan
   const int32_t qpt = kTileRows / group;
   const int32_t span = qpt * kTilesPerItem;
   std::vector<PItem> items;
-  std::vector<int64_t> item0(batch, -1);
   int32_t max_k_tiles = 0;
   for (int r = 0; r < batch; ++r) {
     const int32_t t = q_off[r + 1] - q_off[r];
-    if (prior[r] == 0 || t == 0) continue;
-    item0[r] = (int64_t)items.size();
-    const int32_t tiles = (int32_t)(((int64_t)prior[r] + kTileKeys - 1) / kTileKeys);
+    const int32_t tiles = (int32_t)(((int64_t)keys[r] + kTileKeys - 1) / kTileKeys);
     max_k_tiles = std::max(max_k_tiles, tiles);
     for (int32_t q0 = 0; q0 < t; q0 += span)
-      for (int g = 0; g < kv_heads; ++g) items.push_back({r, g, q0, tiles, true, t - q0 <= qpt});
+      for (int g = 0; g < kv_heads; ++g) items.push_back({r, g, q0, tiles, false, t - q0 <= qpt});
   }
-  // few items are cut finely enough to give every SM a few pieces
   const int max_split =
       items.empty() ? 1
                     : (int)std::max<int64_t>(kMaxSplit, 2 * kSmCount / (int64_t)items.size());
-  std::vector<Row4> citems;
+  std::vector<Row4> no_citems;
   Pieces pieces;
-  plan_pieces(items, max_split, citems, pieces);
+  plan_pieces(items, max_split, no_citems, pieces, kTreeMinPieceTiles);
   if (pieces.work.size() > (size_t)kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
 
   // ---- layout
@@ -139,10 +135,9 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   p.off_seg_kstart = lay.take(nseg);
   p.off_seg_len = lay.take(nseg);
   p.off_work = lay.take(kWorkInts * (int64_t)pieces.work.size());
-  desc->off_row = lay.take(8 * total_q);
+  p.off_merge = lay.take(8 * (int64_t)pieces.merge.size());
   desc->off_mask = lay.take((int64_t)words.size());
   desc->off_draft_slot = lay.take(total_q);
-  desc->off_citem = lay.take(4 * (int64_t)citems.size());
 
   p.magic = SEG_ATTN_TABLE_MAGIC;
   p.version = SEG_ATTN_TABLE_VERSION;
@@ -158,6 +153,7 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   p.num_work = (int32_t)pieces.work.size();
   p.queries_per_tile = qpt;
   p.max_k_tiles = max_k_tiles;
+  p.num_merge = (int32_t)pieces.merge.size();
   p.num_parts = pieces.slots;
   p.num_single = pieces.single;
   desc->magic = SEG_ATTN_TREE_MAGIC;
@@ -179,7 +175,7 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   std::vector<int32_t> seg_off(batch + 1, 0);
   int32_t s0 = 0;
   for (int r = 0; r < batch; ++r) {
-    t[p.off_k_lens + r] = prior[r];
+    t[p.off_k_lens + r] = keys[r];
     int32_t logical = 0;
     for (size_t s = 0; s < own[r].len.size(); ++s, ++s0) {
       t[p.off_seg_start + s0] = own[r].start[s];
@@ -189,27 +185,19 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
     }
     seg_off[r + 1] = s0;
     t[p.off_seg_offsets + r + 1] = s0;
-    const int32_t n = q_off[r + 1] - q_off[r], nw = (n + 31) / 32;
-    for (int32_t i = 0; i < n; ++i) {
-      int32_t* row = t + desc->off_row + 8 * ((int64_t)q_off[r] + i);
-      const int64_t at = desc->off_mask + mask_at[r] + (int64_t)i * nw;
-      row[0] = q_off[r];
-      row[1] = nw;
-      row[2] = (int32_t)(uint32_t)(at & 0xffffffff);
-      row[3] = (int32_t)(at >> 32);
-      const int32_t block = i / span, local = i - block * span;
-      row[4] = item0[r] < 0 ? -1 : pieces.citem[item0[r] + (int64_t)block * kv_heads];
-      row[5] = (local / qpt) * kTileRows + (local % qpt) * group;
-    }
   }
-  fill_request_words(pieces.work, q_off, prior, own, seg_off);
-  for (size_t i = 0; i < pieces.work.size(); ++i)
+  fill_request_words(pieces.work, q_off, keys, own, seg_off);
+  for (size_t i = 0; i < pieces.work.size(); ++i) {
+    const int64_t at = desc->off_mask + mask_at[pieces.work[i][0]];
+    pieces.work[i][13] = (int32_t)(uint32_t)(at & 0xffffffff);
+    pieces.work[i][14] = (int32_t)(at >> 32);
     memcpy(t + p.off_work + kWorkInts * i, pieces.work[i].data(), kWorkInts * sizeof(int32_t));
+  }
+  for (size_t i = 0; i < pieces.merge.size(); ++i)
+    memcpy(t + p.off_merge + 8 * i, pieces.merge[i].data(), 8 * sizeof(int32_t));
   if (!words.empty()) memcpy(t + desc->off_mask, words.data(), words.size() * sizeof(uint32_t));
   if (!draft_slot.empty())
     memcpy(t + desc->off_draft_slot, draft_slot.data(), draft_slot.size() * sizeof(int32_t));
-  for (size_t i = 0; i < citems.size(); ++i)
-    memcpy(t + desc->off_citem + 4 * i, citems[i].data(), 4 * sizeof(int32_t));
   return SEG_ATTN_OK;
 }
 

@@ -148,11 +148,6 @@ def test_small_buffer_and_null_desc(lib):
     assert lib.seg_attn_build_tree_table(*args, P(at), need, ctypes.byref(desc)) == 0
 
 
-def words_of(tab, n):
-    d = tab.desc
-    return tab.host[d.off_row: d.off_row + 8 * n].view(-1, 8).tolist()
-
-
 @pytest.mark.parametrize("seed", range(6))
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (64, 8), (128, 1), (3, 3)])
 def test_tree_table_content(seed, hq, hkv):
@@ -170,42 +165,43 @@ def test_tree_table_content(seed, hq, hkv):
     tab = sa.TreeTable.build(draft, c["seg_starts"], c["seg_lens"], c["num_slots"], hq, hkv, 64, **kw)
     vis = ref.visible(draft, **kw)
     d, p, host = tab.desc, tab.desc.pass_, tab.host
-    rows = words_of(tab, sum(draft))
     slot = host[d.off_draft_slot: d.off_draft_slot + sum(draft)].tolist()
     G = hq // hkv
     qpt = 128 // G
     work = host[p.off_work: p.off_work + 16 * p.num_work].view(-1, 16).tolist()
-    pieces = {}
+    merge = host[p.off_merge: p.off_merge + 8 * p.num_merge].view(-1, 8).tolist()
+    items = {}
     for w in work:
-        pieces.setdefault((w[0], w[1], w[2]), []).append((w[5], w[3], w[4]))
-    seen_slots, at = [], 0
+        items.setdefault((w[0], w[1], w[2]), []).append(w)
+    slots_used, at = [], 0
     for r, t in enumerate(draft):
         keys = [s + i for s, l in zip(c["seg_starts"][r], c["seg_lens"][r]) for i in range(l)]
         assert slot[at:at + t] == keys[prior[r]:]
-        for i in range(t):
-            w = rows[at + i]
-            assert w[0] == at and w[1] == (t + 31) // 32
-            m0 = (w[2] & 0xffffffff) | (w[3] << 32)
-            bits = [x & 0xffffffff for x in host[m0:m0 + w[1]].tolist()]
-            assert [bool(bits[j >> 5] >> (j & 31) & 1) for j in range(t)] == vis[r][i].tolist()
-            if prior[r] == 0:
-                assert w[4] == -1
-                continue
-            block, local = divmod(i, 2 * qpt)
-            assert w[5] == (local // qpt) * 128 + (local % qpt) * G
+        tiles, nw = (len(keys) + 127) // 128, (t + 31) // 32
+        for q0 in range(0, t, 2 * qpt):
             for g in range(hkv):
-                slot0, n, q0, _ = host[d.off_citem + 4 * (w[4] + g):][:4].tolist()
-                assert q0 == block * 2 * qpt
-                # the item's pieces: consecutive slots over all of its K tiles
-                got = sorted(pieces[(r, g, q0)])
-                assert [x[0] for x in got] == list(range(slot0, slot0 + n))
-                assert got[0][1] == 0 and got[-1][2] == (prior[r] + 127) // 128
-                assert all(a[2] == b[1] for a, b in zip(got, got[1:]))
-                seen_slots += [x[0] for x in got] if local == 0 else []
+                got = sorted(items.pop((r, g, q0)), key=lambda w: w[3])
+                # the item's pieces cover all of its K tiles
+                assert got[0][3] == 0 and got[-1][4] == tiles
+                assert all(x[4] == y[3] for x, y in zip(got, got[1:]))
+                if len(got) == 1:
+                    assert got[0][5] == -1
+                else:
+                    row = [m for m in merge if m[:3] == [r, g, q0]]
+                    assert len(row) == 1 and row[0][4] == len(got)
+                    assert [w[5] for w in got] == [row[0][3] + i for i in range(len(got))]
+                    slots_used += [w[5] for w in got]
+                for w in got:
+                    assert w[8:11] == [at, t, len(keys)]
+                    m0 = (w[13] & 0xffffffff) | (w[14] << 32)
+                    bits = [x & 0xffffffff for x in host[m0:m0 + t * nw].tolist()]
+                    for i in range(t):
+                        row_bits = bits[i * nw:(i + 1) * nw]
+                        assert [bool(row_bits[j >> 5] >> (j & 31) & 1) for j in range(nw * 32)] == \
+                            vis[r][i].tolist() + [False] * (nw * 32 - t)
         at += t
-    assert sorted(seen_slots) == list(range(p.num_parts)) and p.num_parts == p.num_work
-    if p.num_work:
-        assert tab.workspace_bytes >= p.num_parts * 256 * (64 + 1) * 4
+    assert not items and sorted(slots_used) == list(range(p.num_parts))
+    assert p.num_parts == 0 or tab.workspace_bytes >= p.num_parts * 256 * (64 + 1) * 4
 
 
 def test_empty_batches():

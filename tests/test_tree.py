@@ -124,12 +124,14 @@ def test_rows_that_see_nothing(fp8):
 def test_masked_rows_may_hold_anything(value):
     """What a token does not see never reaches its row; V's NaN and infinities reach those that
     see them."""
-    draft, prior = [6, 5], [130, 0]
-    parents = [-1, 0, 0, 1, 2, 4, -1, -1, 1, 2, 2]
-    c = ref.tree_case(random.Random(7), draft, prior, 16, 2, 128)
+    rnd = random.Random(7)
+    draft, prior = [6, 5, 50, 150], [130, 0, 4000, 60]
+    parents = [-1, 0, 0, 1, 2, 4, -1, -1, 1, 2, 2] + [p for t in draft[2:] for p in
+                                                      ref.random_parents(rnd, t)]
+    c = ref.tree_case(rnd, draft, prior, 16, 2, 128)
     clean, clean_lse = check(c, parents=parents)
     vis = ref.visible(draft, parents=parents)
-    for r, j in ((0, 1), (0, 5), (1, 0), (1, 2)):
+    for r, j in ((0, 1), (0, 5), (1, 0), (1, 2), (2, 0), (2, 33), (3, 10), (3, 67), (3, 149)):
         keys = [s + i for s, l in zip(c["seg_starts"][r], c["seg_lens"][r]) for i in range(l)]
         slot = keys[prior[r] + j]
         for name in ("k_pool", "v_pool"):
@@ -142,6 +144,8 @@ def test_masked_rows_may_hold_anything(value):
             sees[at:at + draft[r]] = torch.from_numpy(vis[r][:, j])
             sees = sees.cuda()
             assert torch.equal(out[~sees], clean[~sees]) and torch.equal(lse[~sees], clean_lse[~sees])
+            if math.isinf(value) and name == "v_pool":
+                assert bool((out[sees] == value).all())
             if math.isnan(value):
                 assert bool(torch.isnan(out[sees]).all())
                 assert torch.isnan(lse[sees]).all() if name == "k_pool" else \
@@ -168,7 +172,7 @@ def test_two_streams_with_workspaces_of_their_own():
     outs = []
     for c, tab, s in zip((c1, c2), tabs, streams):
         with torch.cuda.stream(s):
-            ws = torch.empty(tab.workspace_bytes, dtype=torch.uint8, device="cuda")
+            ws = torch.empty(max(16, tab.workspace_bytes), dtype=torch.uint8, device="cuda")
             outs.append([run(c, tab, ws=ws) for _ in range(6)])
     torch.cuda.synchronize()
     for runs, (o, l) in zip(outs, want):
@@ -180,7 +184,7 @@ def test_captured_and_replayed_with_new_values():
     c = ref.tree_case(random.Random(11), [7, 12], [900, 260], 16, 2, 128)
     parents = [-1, 0, 0, 1, 1, 2, 3] + [i - 1 for i in range(12)]
     tab = table(c, parents=parents)
-    ws = torch.empty(tab.workspace_bytes, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(16, tab.workspace_bytes), dtype=torch.uint8, device="cuda")
     out, lse = torch.empty_like(c["q"]), torch.empty(19, 16, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -197,9 +201,10 @@ def test_captured_and_replayed_with_new_values():
 
 
 def test_binding_refuses_wrong_tensors():
-    c = ref.tree_case(random.Random(12), [3], [10], 4, 2, 64)
+    c = ref.tree_case(random.Random(12), [3], [3000], 4, 2, 64)
     tab = table(c)
     out, lse = torch.empty_like(c["q"]), torch.empty(3, 4, device="cuda")
+    assert tab.workspace_bytes > 0
     ws = torch.empty(max(16, tab.workspace_bytes), dtype=torch.uint8, device="cuda")
     good = dict(q=c["q"], k_pool=c["k_pool"], v_pool=c["v_pool"], out=out, lse=lse,
                 dev_table=tab.device, desc=tab.desc, softmax_scale=0.1, workspace=ws)
@@ -377,3 +382,35 @@ def test_draft_verify_commit_steps(fp8):
         assert len(got) == len(truth[r]) == lens[r]
         assert all(torch.equal(a, x) and torch.equal(b, y) for (a, b), (x, y) in zip(got, truth[r]))
     assert sa.seg_attn_take_device_error() == 0
+
+
+def test_masked_nan_codes_in_an_e4m3_cache():
+    """E4M3 has NaN codes only: a drafted V row with some reaches the rows that see it, in those
+    columns, and no others; a K row with some never reaches rows that do not see it."""
+    rnd = random.Random(13)
+    draft, prior = [9, 40], [300, 0]
+    parents = [p for t in draft for p in ref.random_parents(rnd, t)]
+    c = ref.tree_case(rnd, draft, prior, 64, 8, 128, fp8=True)
+    clean, clean_lse = check(c, parents=parents)
+    vis = ref.visible(draft, parents=parents)
+    for r, j in ((0, 0), (0, 7), (1, 3), (1, 39)):
+        keys = [s + i for s, l in zip(c["seg_starts"][r], c["seg_lens"][r]) for i in range(l)]
+        slot = keys[prior[r] + j]
+        at = sum(draft[:r])
+        sees = torch.zeros(sum(draft), dtype=torch.bool)
+        sees[at:at + draft[r]] = torch.from_numpy(vis[r][:, j])
+        sees = sees.cuda()
+        for name, code in (("v_pool", 0x7F), ("v_pool", 0xFF), ("k_pool", 0x7F)):
+            keep = c[name][slot].clone()
+            c[name][slot, 2, 5] = code
+            out, lse = run(c, table(c, parents=parents))
+            c[name][slot] = keep
+            same = (out == clean)
+            hit = torch.zeros_like(same)
+            if name == "v_pool":
+                hit[sees, 16:24, 5] = True          # the 8 query heads of kv head 2
+                assert torch.equal(lse, clean_lse)
+            else:
+                hit[sees, 16:24] = True
+                assert torch.equal(torch.isnan(lse), hit[..., 0])
+            assert bool(same[~hit].all()) and bool(torch.isnan(out[hit]).all())
