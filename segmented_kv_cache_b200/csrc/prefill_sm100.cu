@@ -209,20 +209,21 @@ __device__ __forceinline__ void widen_tile_in_place(uint8_t* slot, int ct) {
   ptx::named_barrier(1, NT);
   const int sw = r0 & 7, c0 = (j & 3) * 2;
   uint8_t* d = slot + (j >> 2) * kHalfBytes + r0 * 128;
-  const int o0 = (c0 ^ sw) << 4, o1 = ((c0 + 1) ^ sw) << 4;
+  // the eight lanes of a row hold columns of both 64-column halves, whose chunks share
+  // banks: the second half's lanes store their odd chunk first, so that the eight stores
+  // of each instruction fall on eight different 16-byte banks
+  const bool odd = (j >> 2) != 0;
+  const int o0 = ((c0 + (odd ? 1 : 0)) ^ sw) << 4, o1 = ((c0 + (odd ? 0 : 1)) ^ sw) << 4;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    uint4 lo, hi;
-    lo.x = ptx::e4m3x2_to_f16x2(w[k].x);
-    lo.y = ptx::e4m3x2_to_f16x2(w[k].x >> 16);
-    lo.z = ptx::e4m3x2_to_f16x2(w[k].y);
-    lo.w = ptx::e4m3x2_to_f16x2(w[k].y >> 16);
-    hi.x = ptx::e4m3x2_to_f16x2(w[k].z);
-    hi.y = ptx::e4m3x2_to_f16x2(w[k].z >> 16);
-    hi.z = ptx::e4m3x2_to_f16x2(w[k].w);
-    hi.w = ptx::e4m3x2_to_f16x2(w[k].w >> 16);
-    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o0) = lo;
-    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o1) = hi;
+    const uint32_t a0 = odd ? w[k].z : w[k].x, a1 = odd ? w[k].w : w[k].y;
+    const uint32_t b0 = odd ? w[k].x : w[k].z, b1 = odd ? w[k].y : w[k].w;
+    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o0) =
+        make_uint4(ptx::e4m3x2_to_f16x2(a0), ptx::e4m3x2_to_f16x2(a0 >> 16),
+                   ptx::e4m3x2_to_f16x2(a1), ptx::e4m3x2_to_f16x2(a1 >> 16));
+    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o1) =
+        make_uint4(ptx::e4m3x2_to_f16x2(b0), ptx::e4m3x2_to_f16x2(b0 >> 16),
+                   ptx::e4m3x2_to_f16x2(b1), ptx::e4m3x2_to_f16x2(b1 >> 16));
   }
 }
 
@@ -298,6 +299,13 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
   // second S buffer of tile 0, so the next tile's S = QK^T overlaps this tile's
   // softmax.
   constexpr bool single = SINGLE;
+  // TREE, item with queries in query tile 0 only (row word 6): both softmax groups work
+  // on that tile, group t on K tiles t, t + 2, ... with an O of its own, and the two are
+  // merged at the end.  (One group alone takes ~3200 cycles per K tile, exponentials,
+  // packing and tensor-memory round trips in series, where the K/V bytes of a tile
+  // arrive in 2600 over a bf16 cache and 1300 over an E4M3 one.)
+  const bool dual = TREE && w1.z != 0;
+  const int ahead = dual ? 2 : 1;  // K tiles go out this many before their V tile
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       // (a stage of the fresh ring is free)
       const bool k0_early = !FP8 && w3.x >= 0 && p.withhold_tile != 0;
       if (lane == 0) {
-        const int q_tiles = single ? 1 : 2;
+        const int q_tiles = single || dual ? 1 : 2;
         mbar_expect_tx(q_full, q_tiles * TILE);
         for (int t = 0; t < q_tiles; ++t)
           for (int h = 0; h < HALVES; ++h)
@@ -456,18 +464,23 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
         ++v_issued;
         return true;
       };
-      // K tile i + 1 before V tile i: the MMA warp takes them in that order
-      TileRows cur, nxt;
+      // K tile i + 1 (dual: i + 2) before V tile i: the MMA warp takes them in that order
+      TileRows cur, nxt, far;
       tile_rows(0, cur);
       if (k0_early) ++k_issued;
       bool run = k0_early || load_k(0, cur);
+      if (dual && n_tiles > 1) {
+        tile_rows(1, nxt);
+        run = run && load_k(1, nxt);
+      }
       for (int i = 0; run && i < n_tiles; ++i) {
-        if (i + 1 < n_tiles) {
-          tile_rows(i + 1, nxt);
-          if (!(run = load_k(i + 1, nxt))) break;
+        if (i + ahead < n_tiles) {
+          tile_rows(i + ahead, far);
+          if (!(run = load_k(i + ahead, far))) break;
         }
         if (!(run = load_v(i, cur))) break;
-        cur = nxt;
+        cur = dual ? nxt : far;
+        nxt = far;
       }
       // never leave the CTA with copies in flight (the copies' own barriers:
       // over an FP8 cache the slots' full barriers wait for the widening threads too)
@@ -585,6 +598,35 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
             mma_commit_warp(k_empty + ks);
           }
         }
+      } else if (dual) {
+        // One query tile, two softmax groups, one S buffer.  Use i of the buffer is QK of
+        // K tile i, for group i & 1; it may start once the other group has read use i - 1
+        // (completion i - 1 of s_free).  Order: QK(i + 2), PV(i), with P and O of the group.
+        for (int i = 0; ok && i < 2 && i < n_tiles; ++i) {
+          if (i > 0 && !(ok = wait_all(k_full + i, 0) && wait_all(s_free, 0))) break;
+          tc_fence_after();
+          issue_qk_t(0, i);
+          mma_commit_warp(s_full + i);
+          mma_commit_warp(k_empty + i);
+        }
+        for (int i = 0; ok && i < n_tiles; ++i) {
+          const int g2 = i & 1, st = i % RV;
+          if (i + 2 < n_tiles) {
+            const int st2 = (i + 2) % RK;
+            if (!(ok = wait_all(k_full + st2, ((i + 2) / RK) & 1) && wait_all(s_free, (i + 1) & 1)))
+              break;
+            tc_fence_after();
+            issue_qk_t(0, st2);
+            mma_commit_warp(s_full + g2);
+            mma_commit_warp(k_empty + st2);
+          }
+          if (!(ok = wait_all(v_full + st, (i / RV) & 1) && wait_all(p_full + g2, (i >> 1) & 1)))
+            break;
+          tc_fence_after();
+          issue_pv_s(g2, st, i > 1);
+          mma_commit_warp(o_full + g2);
+          mma_commit_warp(v_empty + st);
+        }
       } else {
         // Two tiles, one S buffer.  Use u of the buffer is QK of K tile u / 2 for
         // query tile u % 2; it may start once the softmax has read use u - 1
@@ -651,8 +693,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     // visible to the tensor cores before signalling the ring slot full.
     const int ct = threadIdx.x - kConvWarp0 * 32;
     bool ok = true;
-    // codes in the slot's second half, in the producer's order: K tile 0, then K tile
-    // i + 1 before V tile i.  The widening threads agree on every wait's outcome at a
+    // codes in the slot's second half, in the producer's order.  The widening threads agree on every wait's outcome at a
     // barrier (all or none go on), since the widening meets at another one.
     auto widen = [&](uint8_t* slot, uint64_t* landed, uint32_t parity, uint64_t* full) -> bool {
       const bool got = mbar_wait(landed, parity, abort_flag, wait_limit);
@@ -662,11 +703,12 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       mbar_arrive(full);
       return true;
     };
-    if (n_tiles > 0) ok = widen(sK, code_k, 0, k_full);
+    for (int i = 0; ok && i < ahead && i < n_tiles; ++i)
+      ok = widen(sK + i * TILE, code_k + i, 0, k_full + i);
     for (int i = 0; ok && i < n_tiles; ++i) {
-      if (i + 1 < n_tiles) {
-        const int sk = (i + 1) % RK;
-        if (!(ok = widen(sK + sk * TILE, code_k + sk, ((i + 1) / RK) & 1, k_full + sk))) break;
+      if (i + ahead < n_tiles) {
+        const int nk = i + ahead, sk = nk % RK;
+        if (!(ok = widen(sK + sk * TILE, code_k + sk, (nk / RK) & 1, k_full + sk))) break;
       }
       const int sv = i % RV;
       ok = widen(sV + sv * TILE, code_v + sv, (i / RV) & 1, v_full + sv);
@@ -676,7 +718,8 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     const int t = (warp - 2) >> 2;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
-    const int qi = q0 + t * p.qpt + row / p.group;
+    const int tq = dual ? 0 : t;  // query tile of this group's rows
+    const int qi = q0 + tq * p.qpt + row / p.group;
     const int head = g * p.group + row % p.group;
     const bool row_valid = qi < q_len;
     const int prior = k_len - q_len;  // TREE: keys before the drafted ones
@@ -706,6 +749,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     uint32_t tP = lane_base + 384 + 64 * t;
     // FP8: scores are q . code * k_scale, so the K scale joins the softmax scale
     const float sl2 = FP8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
+    const int my_tiles = dual ? (n_tiles - t + 1) >> 1 : n_tiles;  // K tiles of this group
     float m_ref = -INFINITY;  // raw score units
     float l = 0.f;
     // a row that saw a NaN score has a NaN sum, which its lse shows (drafted tokens)
@@ -718,16 +762,18 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       // 32 rows over all shared-memory banks.
       ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, wait_limit));
       if (ok) {
+        if (!dual || t == 0) {
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h)
+          for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint4* chunk = reinterpret_cast<uint4*>(sQ + t * QSTRIDE + h * kHalfBytes + row * 128 +
-                                                    ((c ^ (row & 7)) << 4));
-            uint4 v = *chunk;
-            bf16x8_to_f16x8(v);
-            *chunk = v;
-          }
+            for (int c = 0; c < 8; ++c) {
+              uint4* chunk = reinterpret_cast<uint4*>(sQ + t * QSTRIDE + h * kHalfBytes +
+                                                      row * 128 + ((c ^ (row & 7)) << 4));
+              uint4 v = *chunk;
+              bf16x8_to_f16x8(v);
+              *chunk = v;
+            }
+        }
         fence_proxy_async_smem();
         mbar_arrive(q_conv);
       }
@@ -735,7 +781,8 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     // One tile of the online softmax.  `masked`: some row of the warp must not
     // see some key of the tile (causal diagonal, end of the request); the mask
     // is applied to the registers, so other tiles never compare per element.
-    auto softmax_tile = [&](int i, bool masked) -> bool {
+    // K tile i is this group's j-th (i = j unless dual).
+    auto softmax_tile = [&](int i, int j, bool masked) -> bool {
       auto f = [](uint32_t bits) { return __uint_as_float(bits); };
       // the whole S row in registers: one round trip to tensor memory
       uint32_t sv[4][32];
@@ -789,9 +836,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       // PV(i - 1) has read it (complete by now as a rule: it was issued when this
       // tile's S was)
       bool waited = false;
-      if (QT && i > 0) {
+      if (QT && j > 0) {
         if (!__all_sync(0xffffffffu,
-                        mbar_wait(o_full + t, (i - 1) & 1, abort_flag, wait_limit, true)))
+                        mbar_wait(o_full + t, (j - 1) & 1, abort_flag, wait_limit, true)))
           return false;
         tc_fence_after();
         waited = true;
@@ -821,9 +868,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       if constexpr (QT) f2_unpack(ls, ls0, ls1);
       l = l * alpha + (ls0 + ls1);
       if (__any_sync(0xffffffffu, rescale)) {
-        // O_t holds PV up to K tile i - 1; rescale it in place once that is complete
+        // O_t holds PV up to this group's tile j - 1; rescale it in place once that is complete
         if (!waited &&
-            !__all_sync(0xffffffffu, mbar_wait(o_full + t, (i - 1) & 1, abort_flag, wait_limit)))
+            !__all_sync(0xffffffffu, mbar_wait(o_full + t, (j - 1) & 1, abort_flag, wait_limit)))
           return false;
         tc_fence_after();
 #pragma unroll
@@ -854,7 +901,8 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     };
     // TREE, tile with drafted keys: V row `row` of the tile, when it is a drafted key's (or
     // past the last key), gets zeros for values that are not finite.  Query tile 0's
-    // threads do it before they signal P; the PV of tile 1 is issued after tile 0's.
+    // threads (dual: the group that has the K tile) do it before they signal P; the PV of
+    // query tile 1 is issued after tile 0's.
     auto clean_v = [&](int i) -> bool {
       const int sv = i % RV;
       if (!__all_sync(0xffffffffu, mbar_wait(v_full + sv, (i / RV) & 1, abort_flag, wait_limit)))
@@ -886,7 +934,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       return true;
     };
     // one K tile of softmax on S buffer sb (phase sph of its barriers)
-    auto run_tile = [&](int i, int sb, uint32_t sph) -> bool {
+    auto run_tile = [&](int i, int j, int sb, uint32_t sph) -> bool {
       if (single) {
         tS = lane_base + 256 + 128 * sb;
         tP = lane_base + 128 + 64 * sb;
@@ -899,21 +947,21 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
           // arrivals never count towards the previous P
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free);
-          if (i > 0 &&
-              !__all_sync(0xffffffffu, mbar_wait(o_full + t, (i - 1) & 1, abort_flag, wait_limit)))
+          if (j > 0 &&
+              !__all_sync(0xffffffffu, mbar_wait(o_full + t, (j - 1) & 1, abort_flag, wait_limit)))
             return false;
         }
         if (!last_pv_order(i)) return false;
-        if (TREE && t == 0 && (kt0 + i + 1) * kTileKeys > prior && !clean_v(i)) return false;
+        if (TREE && tq == 0 && (kt0 + i + 1) * kTileKeys > prior && !clean_v(i)) return false;
         mbar_arrive(p_full + sb);
         return true;
       }
       tc_fence_after();
       const bool masked = __any_sync(0xffffffffu, (kt0 + i + 1) * kTileKeys > vis);
-      if (!softmax_tile(i, masked)) return false;
+      if (!softmax_tile(i, j, masked)) return false;
       tmem_wait_st();
       if (!last_pv_order(i)) return false;
-      if (TREE && t == 0 && masked && !clean_v(i)) return false;
+      if (TREE && tq == 0 && masked && !clean_v(i)) return false;
       tc_fence_before();
       mbar_arrive(p_full + sb);
       return true;
@@ -922,18 +970,18 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       // S buffers alternate; unrolled by two so each buffer's address is fixed
       for (int i = 0; ok && i < n_tiles; i += 2) {
         const uint32_t sph = (i >> 1) & 1;
-        ok = run_tile(i, 0, sph);
-        if (ok && i + 1 < n_tiles) ok = run_tile(i + 1, 1, sph);
+        ok = run_tile(i, i, 0, sph);
+        if (ok && i + 1 < n_tiles) ok = run_tile(i + 1, i + 1, 1, sph);
       }
     } else {
-      for (int i = 0; ok && i < n_tiles; ++i) ok = run_tile(i, t, i & 1);
+      for (int j = 0; ok && j < my_tiles; ++j)
+        ok = run_tile(dual ? 2 * j + t : j, j, t, j & 1);
     }
     // order test (one tile): the last PV completes before this warp reaches the end
     // of the item
     if constexpr (SINGLE) {
       if (p.p_delay_ns > 0 && ok) __nanosleep(p.p_delay_ns);
     }
-    if (!warp_live) ok = false;  // nothing to write
     // TREE, after some drafted V value was not finite: what this row sees of them is added
     // to O in tensor memory, as its product with a positive weight would be (a NaN or an
     // infinity).  32 columns at a time, every lane of the warp in step.
@@ -947,6 +995,8 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
         tmem_wait_ld(o);
 #pragma unroll 1
         for (int j = first; j < last; ++j) {
+          // dual: drafted keys in this group's K tiles
+          if (dual && ((((prior + j) / kTileKeys) ^ kt0 ^ t) & 1)) continue;
           const bool seen = mask_word(j) & 1u;
           const int64_t at =
               ((int64_t)__ldg(p.draft_slot + tok0 + j) * p.kv_heads + g) * D + 32 * c;
@@ -966,6 +1016,12 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       }
       tmem_wait_st();
     };
+    // dual: weight of this group's O and of the other group's, whose O waits in shared
+    // memory (in the K ring, which is free then) as [16-byte chunk][row]
+    float w_own = 1.f, w_other = 0.f;
+    float4* other_o = reinterpret_cast<float4*>(sK);
+    float2* other_ml = reinterpret_cast<float2*>(sK + 128 * D * 4);
+    static_assert(!TREE || 128 * D * 4 + 128 * 8 <= RK * TILE, "exchange fits the K ring");
     // this row's O (fp32, D columns) in registers: every load issued, one wait
     auto load_o = [&](uint32_t (&o)[D / 32][32]) {
       if (n_tiles > 0) {
@@ -985,13 +1041,54 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[c][e] = 0u;
       }
+      if (TREE && w_other != 0.f) {
+#pragma unroll
+        for (int c = 0; c < D / 4; ++c) {
+          const float4 x = other_o[c * 128 + row];
+          uint32_t* y = &o[c / 8][4 * (c % 8)];
+          y[0] = __float_as_uint(__uint_as_float(y[0]) * w_own + x.x * w_other);
+          y[1] = __float_as_uint(__uint_as_float(y[1]) * w_own + x.y * w_other);
+          y[2] = __float_as_uint(__uint_as_float(y[2]) * w_own + x.z * w_other);
+          y[3] = __float_as_uint(__uint_as_float(y[3]) * w_own + x.w * w_other);
+        }
+      }
     };
     // PV complete up to tile n - 2 (two tiles: P(n - 1) was written after it; one
     // tile: confirmed before P(n - 1) was signalled), so o_full is at completion
     // n - 1 or n and a parity wait for PV(n - 1) is unambiguous
-    if (ok && n_tiles > 0)
+    if (ok && my_tiles > 0)
       ok = __all_sync(0xffffffffu,
-                      mbar_wait(o_full + t, (n_tiles - 1) & 1, abort_flag, wait_limit));
+                      mbar_wait(o_full + t, (my_tiles - 1) & 1, abort_flag, wait_limit));
+    if (dual) {
+      // Group 1 hands its state over and is done.  All of the item's QK are complete once
+      // its last PV is (QK of the last K tile is issued before it), so the K ring is free.
+      // Both groups meet at an AND of their outcomes, so a give-up leaves no one waiting.
+      if (t == 1 && ok && my_tiles > 0) {
+        if (warp_live) {
+          uint32_t o[D / 32][32];
+          load_o(o);
+#pragma unroll
+          for (int c = 0; c < D / 4; ++c) {
+            const uint32_t* y = &o[c / 8][4 * (c % 8)];
+            other_o[c * 128 + row] = make_float4(__uint_as_float(y[0]), __uint_as_float(y[1]),
+                                                 __uint_as_float(y[2]), __uint_as_float(y[3]));
+          }
+        }
+        other_ml[row] = make_float2(m_ref, l);
+      }
+      ok = named_barrier_and(4, 256, ok);
+      if (t == 1) ok = false;  // nothing to write
+      if (ok && n_tiles > 1) {
+        const float2 ml = other_ml[row];
+        const float top = fmaxf(m_ref, ml.x);
+        // a group that saw no key has a zero O (and m = -inf): its weight must not be NaN
+        w_own = m_ref == top ? 1.f : ex2((m_ref - top) * sl2);
+        w_other = ml.x == top ? 1.f : ex2((ml.x - top) * sl2);
+        l = l * w_own + ml.y * w_other;
+        m_ref = top;
+      }
+    }
+    if (!warp_live) ok = false;  // nothing to write
     // Results leave through shared memory so that whole rows are stored: a thread
     // owns one row, and its own 16-byte pieces of it would put every warp store on 32
     // different lines.  The tile's query region is free (the commit of the tile's
@@ -1301,9 +1398,12 @@ int launch_prefill_d(const PrefillLaunch& a, cudaStream_t stream) {
     const int rc = any_final ? launch(F{}, T{}, 0, n_two) : launch(F{}, F{}, 0, n_two);
     if (rc != SEG_ATTN_OK) return rc;
   }
-  if (n_single > 0) {
-    const int rc = any_final ? launch(T{}, T{}, n_two, n_single) : launch(T{}, F{}, n_two, n_single);
-    if (rc != SEG_ATTN_OK) return rc;
+  if constexpr (!TREE) {  // drafted tokens: one-tile items run both ways in one launch
+    if (n_single > 0) {
+      const int rc =
+          any_final ? launch(T{}, T{}, n_two, n_single) : launch(T{}, F{}, n_two, n_single);
+      if (rc != SEG_ATTN_OK) return rc;
+    }
   }
   if (!TREE && d.num_merge > 0) {
     prefill_merge_kernel<D><<<dim3(d.num_merge, 4), 256, 0, stream>>>(p);

@@ -153,8 +153,9 @@ int tree(const void* q, const void* k_pool, const void* v_pool, const float* k_s
   m.q_heads = pass.q_heads;
   m.group = pass.q_heads / pass.kv_heads;
   m.qpt = pass.queries_per_tile;
-  // a pass of one-tile items has no rows past the first tile
-  const dim3 grid(pass.num_merge, (pass.num_single == pass.num_work ? kTileRows : kItemRows) / 8);
+  // no item has rows past the first tile when every draft fits in it
+  const dim3 grid(pass.num_merge,
+                  (desc->max_draft <= pass.queries_per_tile ? kTileRows : kItemRows) / 8);
   if (pass.head_dim == 128)
     tree_merge_kernel<128><<<grid, 256, 0, st>>>(m);
   else

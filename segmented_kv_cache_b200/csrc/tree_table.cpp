@@ -115,7 +115,7 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
     const int32_t tiles = (int32_t)(((int64_t)keys[r] + kTileKeys - 1) / kTileKeys);
     max_k_tiles = std::max(max_k_tiles, tiles);
     for (int32_t q0 = 0; q0 < t; q0 += span)
-      for (int g = 0; g < kv_heads; ++g) items.push_back({r, g, q0, tiles, false, t - q0 <= qpt});
+      for (int g = 0; g < kv_heads; ++g) items.push_back({r, g, q0, tiles, false, false});
   }
   const int max_split =
       items.empty() ? 1
@@ -155,7 +155,6 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   p.max_k_tiles = max_k_tiles;
   p.num_merge = (int32_t)pieces.merge.size();
   p.num_parts = pieces.slots;
-  p.num_single = pieces.single;
   desc->magic = SEG_ATTN_TREE_MAGIC;
   desc->version = SEG_ATTN_TREE_VERSION;
   desc->batch = batch;
@@ -189,6 +188,8 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   fill_request_words(pieces.work, q_off, keys, own, seg_off);
   for (size_t i = 0; i < pieces.work.size(); ++i) {
     const int64_t at = desc->off_mask + mask_at[pieces.work[i][0]];
+    // one-tile items: both softmax groups take their one query tile
+    pieces.work[i][6] = q_off[pieces.work[i][0] + 1] - q_off[pieces.work[i][0]] - pieces.work[i][2] <= qpt;
     pieces.work[i][13] = (int32_t)(uint32_t)(at & 0xffffffff);
     pieces.work[i][14] = (int32_t)(at >> 32);
     memcpy(t + p.off_work + kWorkInts * i, pieces.work[i].data(), kWorkInts * sizeof(int32_t));
