@@ -192,39 +192,39 @@ __device__ __forceinline__ void bf16x8_to_f16x8(uint4& v) {
 // ((c ^ (r & 7)) * 16).  Thread ct of the NT widening threads owns one 16-code column j
 // of rows r0, r0 + step, ... with step a multiple of 8, so the swizzle phase r & 7 and
 // both store offsets are fixed per thread and the unrolled loop needs no address
-// arithmetic.  A row's f16 output overwrites code bytes that other threads read, so
-// every thread first loads all of its codes, the NT threads meet at named barrier 1,
-// and only then write.
+// arithmetic.  The eight lanes of a row group hold columns of both halves, whose chunks
+// share banks: the second half's lanes take the neighbouring row (r0 ^ 1), which turns
+// their even chunks into odd ones, so loads and stores are both free of conflicts.
+// A row's f16 output overwrites code bytes that other threads read, so every thread
+// first loads all of its codes, the NT threads meet at named barrier 1, and only then
+// write.  `landed`: this thread saw the copy complete; the barrier makes it the AND of all
+// threads (what was loaded counts only then), which is returned.
 template <int D, int NT>
-__device__ __forceinline__ void widen_tile_in_place(uint8_t* slot, int ct) {
+__device__ __forceinline__ bool widen_tile_in_place(uint8_t* slot, int ct, bool landed) {
   constexpr int kCols = D / 16;
   constexpr int kRowStep = NT / kCols;
   constexpr int kRows = kTileKeys / kRowStep;
   static_assert(kRowStep % 8 == 0, "rows of one thread must share the swizzle phase");
-  const int j = ct % kCols, r0 = ct / kCols;
+  const int j = ct % kCols, r0 = (ct / kCols) ^ (j >> 2);
   const uint8_t* s = slot + (D / 64) * kHalfBytes / 2 + r0 * D + 16 * j;
   uint4 w[kRows];
 #pragma unroll
   for (int k = 0; k < kRows; ++k) w[k] = *reinterpret_cast<const uint4*>(s + k * kRowStep * D);
-  ptx::named_barrier(1, NT);
+  if (!ptx::named_barrier_and(1, NT, landed)) return false;
   const int sw = r0 & 7, c0 = (j & 3) * 2;
   uint8_t* d = slot + (j >> 2) * kHalfBytes + r0 * 128;
-  // the eight lanes of a row hold columns of both 64-column halves, whose chunks share
-  // banks: the second half's lanes store their odd chunk first, so that the eight stores
-  // of each instruction fall on eight different 16-byte banks
-  const bool odd = (j >> 2) != 0;
-  const int o0 = ((c0 + (odd ? 1 : 0)) ^ sw) << 4, o1 = ((c0 + (odd ? 0 : 1)) ^ sw) << 4;
+  const int o0 = (c0 ^ sw) << 4, o1 = ((c0 + 1) ^ sw) << 4;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const uint32_t a0 = odd ? w[k].z : w[k].x, a1 = odd ? w[k].w : w[k].y;
-    const uint32_t b0 = odd ? w[k].x : w[k].z, b1 = odd ? w[k].y : w[k].w;
-    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o0) =
-        make_uint4(ptx::e4m3x2_to_f16x2(a0), ptx::e4m3x2_to_f16x2(a0 >> 16),
-                   ptx::e4m3x2_to_f16x2(a1), ptx::e4m3x2_to_f16x2(a1 >> 16));
-    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o1) =
-        make_uint4(ptx::e4m3x2_to_f16x2(b0), ptx::e4m3x2_to_f16x2(b0 >> 16),
-                   ptx::e4m3x2_to_f16x2(b1), ptx::e4m3x2_to_f16x2(b1 >> 16));
+    uint4 lo, hi;
+    ptx::e4m3x4_to_f16x4(w[k].x, lo.x, lo.y);
+    ptx::e4m3x4_to_f16x4(w[k].y, lo.z, lo.w);
+    ptx::e4m3x4_to_f16x4(w[k].z, hi.x, hi.y);
+    ptx::e4m3x4_to_f16x4(w[k].w, hi.z, hi.w);
+    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o0) = lo;
+    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o1) = hi;
   }
+  return true;
 }
 
 // SINGLE: every item of the launch has queries in its first query tile only
@@ -693,12 +693,12 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     // visible to the tensor cores before signalling the ring slot full.
     const int ct = threadIdx.x - kConvWarp0 * 32;
     bool ok = true;
-    // codes in the slot's second half, in the producer's order.  The widening threads agree on every wait's outcome at a
-    // barrier (all or none go on), since the widening meets at another one.
+    // codes in the slot's second half, in the producer's order.  The widening threads agree on every wait's outcome at
+    // the barrier of the widening (all or none go on).
     auto widen = [&](uint8_t* slot, uint64_t* landed, uint32_t parity, uint64_t* full) -> bool {
-      const bool got = mbar_wait(landed, parity, abort_flag, wait_limit);
-      if (!named_barrier_and(1, kConvThreads, got)) return false;
-      widen_tile_in_place<D, kConvThreads>(slot, ct);
+      const bool got = mbar_try_wait(smem_u32(landed), parity) ||
+                       mbar_wait(landed, parity, abort_flag, wait_limit);
+      if (!widen_tile_in_place<D, kConvThreads>(slot, ct, got)) return false;
       fence_proxy_async_smem();
       mbar_arrive(full);
       return true;

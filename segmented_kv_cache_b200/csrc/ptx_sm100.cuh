@@ -376,6 +376,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
   return y;
 }
 
+// Four E4M3 codes -> four f16 (exact), both halves converted from one register.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+
 // Two fp32 -> f16 pair, round to nearest even (lo in the low half).
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t y;
