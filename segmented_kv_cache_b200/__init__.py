@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -528,7 +529,11 @@ class LATable:
 # ------------------------------------------------- rotary positions and drafted tokens
 # These calls check dtypes, shapes, strides and devices as well, and run on the
 # tensors' device whichever is current (seg_draft.h has the rest of the contract).
+# Their arguments travel as one packed block (csrc/bind.cpp): a decode step makes
+# them with a handful of tokens, where converting 20 arguments one by one costs more
+# than the kernel takes.
 _ROPE_SCALES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4, "per_pair": 5}
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
 
 @dataclass
@@ -551,45 +556,66 @@ def _bad(fn: str, detail: str):
     raise SegAttnError(fn, STATUS["INVALID_ARG"], detail)
 
 
-def _invoke(fn_name: str, device: torch.device, stream, args: tuple) -> None:
+_packers = {}
+
+
+def _packed(fn_name: str, n: int):
+    """(entry point taking one packed block, packer of n 64-bit values) of a call."""
+    got = _packers.get(fn_name)
+    if got is None:
+        fn = getattr(load_library(), fn_name + "_packed")
+        fn.argtypes, fn.restype = [ctypes.c_char_p], ctypes.c_int
+        got = _packers[fn_name] = fn, struct.Struct(f"={n}q").pack
+    return got
+
+
+def _invoke(fn_name: str, device: int, stream, args: tuple) -> None:
     """Call the entry point with ``args`` + the stream, with ``device`` current."""
-    fn = getattr(_lib or load_library(), fn_name)
+    fn, pack = _packed(fn_name, len(args) + 1)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        _bad(fn_name, f"stream on {stream.device}, tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream.cuda_stream)
+        raw = _current_raw_stream(device)
+    elif stream.device.index != device:
+        _bad(fn_name, f"stream on {stream.device}, tensors on cuda:{device}")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        rc = fn(pack(*args, raw))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(pack(*args, raw))
     if rc != 0:
         raise SegAttnError(fn_name, rc)
 
 
-def _ptr(fn: str, name: str, t: torch.Tensor, dtype, device, numel: Optional[int] = None) -> int:
-    """Address of a dense tensor of the given dtype, device and element count."""
-    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or (
-            numel is not None and t.numel() != numel):
-        _bad(fn, f"{name}: a dense {dtype} tensor on {device}"
-                 + (f" of {numel} values" if numel is not None else "")
+# the stream as an integer, without making a Stream object (1 us) where torch has the call
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _ptr(fn: str, name: str, t: torch.Tensor, dtype, device: int, numel: int = -1) -> int:
+    """Address of a dense tensor of the given dtype, device and element count (-1: any)."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or (
+            numel >= 0 and t.numel() != numel):
+        _bad(fn, f"{name}: a dense {dtype} tensor on cuda:{device}"
+                 + (f" of {numel} values" if numel >= 0 else "")
                  + f", not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(fn: str, name: str, t: torch.Tensor, n: int, heads: int, d: int, device):
+def _rows(fn: str, name: str, t: torch.Tensor, shape: tuple, device: int):
     """(address, token stride) of bf16 rows [n, heads, d] with dense heads."""
-    if (t.dtype is not torch.bfloat16 or t.device != device or tuple(t.shape) != (n, heads, d)
-            or (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)):
-        _bad(fn, f"{name}: bf16 [{n}, {heads}, {d}] with dense heads on {device}, "
-                 f"not {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.data_ptr(), t.stride(0)
+    s = t.stride()
+    if (t.dtype is not _BF16 or t.get_device() != device or t.shape != shape
+            or (s[2] != 1 and shape[2] > 1) or (s[1] != shape[2] and shape[1] > 1)):
+        _bad(fn, f"{name}: bf16 {list(shape)} with dense heads on cuda:{device}, "
+                 f"not {t.dtype} {tuple(t.shape)} strides {s} on {t.device}")
+    return t.data_ptr(), s[0]
 
 
-def _cuda_device(fn: str, name: str, t: torch.Tensor, dim: int) -> torch.device:
+def _cuda_device(fn: str, name: str, t: torch.Tensor, dim: int) -> int:
     if not t.is_cuda or t.dim() != dim:
         _bad(fn, f"{name}: a {dim}-dimensional CUDA tensor, not {t.dim()}-dimensional on {t.device}")
-    return t.device
+    return t.get_device()
 
 
 def seg_attn_rope_plan(rotary_dim: int, interleaved: bool = False, base: float = 10000.0,
@@ -618,11 +644,11 @@ def seg_attn_rope(x, out, positions, rope: seg_attn_rope_desc, backward: bool = 
     the angles of ``positions`` (device int32 [n]); ``backward``: the transposed rotation."""
     fn = "seg_attn_rope"
     dev = _cuda_device(fn, "x", x, 3)
-    n, h, d = x.shape
-    xp, xs = _rows(fn, "x", x, n, h, d, dev)
-    op, os_ = _rows(fn, "out", out, n, h, d, dev)
-    pos = _ptr(fn, "positions", positions, torch.int32, dev, n)
-    _invoke(fn, dev, stream, (xp, xs, op, os_, pos, n, h, d, ctypes.byref(rope), int(backward)))
+    shape = x.shape
+    n, h, d = shape
+    _invoke(fn, dev, stream, (*_rows(fn, "x", x, shape, dev), *_rows(fn, "out", out, shape, dev),
+                              _ptr(fn, "positions", positions, _I32, dev, n), n, h, d,
+                              ctypes.addressof(rope), 1 if backward else 0))
 
 
 def _rope_append(fn, q, q_out, k_new, v_new, positions, slots, rope, scales, k_pool, v_pool,
@@ -632,19 +658,23 @@ def _rope_append(fn, q, q_out, k_new, v_new, positions, slots, rope, scales, k_p
     n = k_new.shape[0]
     if (q is None) != (q_out is None):
         _bad(fn, "q and q_out: both or neither")
-    hq = q.shape[1] if q is not None else 0
-    rows = (_rows(fn, "q", q, n, hq, d, dev) + _rows(fn, "q_out", q_out, n, hq, d, dev)
-            if q is not None else (None, 0, None, 0))
-    rows += _rows(fn, "k_new", k_new, n, hk, d, dev) + _rows(fn, "v_new", v_new, n, hk, d, dev)
-    kind = torch.bfloat16 if scales is None else torch.uint8
-    args = rows + (_ptr(fn, "positions", positions, torch.int32, dev, n),
-                   _ptr(fn, "slots", slots, torch.int32, dev, n), n, hq, hk, d,
-                   ctypes.byref(rope))
-    if scales is not None:
-        args += tuple(_ptr(fn, "scales", t, torch.float32, dev, hk) for t in scales)
-    args += (_ptr(fn, "k_pool", k_pool, kind, dev), _ptr(fn, "v_pool", v_pool, kind, dev, S * hk * d),
-             S)
-    _invoke(fn, dev, stream, args)
+    hq = 0
+    rows = (0, 0, 0, 0)
+    if q is not None:
+        if q.dim() != 3:
+            _bad(fn, f"q: [n, heads, d], not {tuple(q.shape)}")
+        hq = q.shape[1]
+        shape = (n, hq, d)
+        rows = (*_rows(fn, "q", q, shape, dev), *_rows(fn, "q_out", q_out, shape, dev))
+    shape = (n, hk, d)
+    kind = _BF16 if scales is None else _U8
+    scale_ptrs = () if scales is None else tuple(
+        _ptr(fn, "scales", t, _F32, dev, hk) for t in scales)
+    _invoke(fn, dev, stream, (
+        *rows, *_rows(fn, "k_new", k_new, shape, dev), *_rows(fn, "v_new", v_new, shape, dev),
+        _ptr(fn, "positions", positions, _I32, dev, n), _ptr(fn, "slots", slots, _I32, dev, n),
+        n, hq, hk, d, ctypes.addressof(rope), *scale_ptrs, _ptr(fn, "k_pool", k_pool, kind, dev),
+        _ptr(fn, "v_pool", v_pool, kind, dev, S * hk * d), S))
 
 
 def seg_attn_rope_append(q, q_out, k_new, v_new, positions, slots, rope: seg_attn_rope_desc,
@@ -727,25 +757,33 @@ class TreeTable:
 def _tree(fn, q, k_pool, v_pool, scales, out, lse, dev_table, desc, softmax_scale, workspace,
           stream):
     dev = _cuda_device(fn, "q", q, 3)
-    p = desc.pass_
-    n, hq, hk, d = p.total_q, p.q_heads, p.kv_heads, p.head_dim
-    kind = torch.bfloat16 if scales is None else torch.uint8
-    pool = p.num_slots * hk * d
-    args = (_ptr(fn, "q", q, torch.bfloat16, dev, n * hq * d),
-            _ptr(fn, "k_pool", k_pool, kind, dev, pool), _ptr(fn, "v_pool", v_pool, kind, dev, pool))
-    if scales is not None:
-        args += tuple(_ptr(fn, "scales", t, torch.float32, dev, hk) for t in scales)
-    args += (_ptr(fn, "out", out, torch.bfloat16, dev, n * hq * d),
-             _ptr(fn, "lse", lse, torch.float32, dev, n * hq) if lse is not None else None,
-             _ptr(fn, "dev_table", dev_table, torch.int32, dev), ctypes.byref(desc),
-             float(softmax_scale))
-    if dev_table.numel() * 4 < desc.table_bytes:
+    sizes = getattr(desc, "_sizes", None)
+    if sizes is None:   # values of q, of lse, of a pool, kv heads, table bytes (read once)
+        p = desc.pass_
+        sizes = desc._sizes = (p.total_q * p.q_heads * p.head_dim, p.total_q * p.q_heads,
+                               p.num_slots * p.kv_heads * p.head_dim, p.kv_heads, desc.table_bytes)
+    nq, nl, pool, hk, table_bytes = sizes
+    kind = _BF16 if scales is None else _U8
+    table = _ptr(fn, "dev_table", dev_table, _I32, dev)
+    if dev_table.numel() * 4 < table_bytes:
         _bad(fn, "dev_table is shorter than the table")
-    if workspace is None:
-        args += (None, 0)
-    else:
-        args += (_ptr(fn, "workspace", workspace, workspace.dtype, dev), workspace.nbytes)
-    _invoke(fn, dev, stream, args)
+    scale_ptrs = () if scales is None else tuple(
+        _ptr(fn, "scales", t, _F32, dev, hk) for t in scales)
+    _invoke(fn, dev, stream, (
+        _ptr(fn, "q", q, _BF16, dev, nq), _ptr(fn, "k_pool", k_pool, kind, dev, pool),
+        _ptr(fn, "v_pool", v_pool, kind, dev, pool), *scale_ptrs,
+        _ptr(fn, "out", out, _BF16, dev, nq),
+        _ptr(fn, "lse", lse, _F32, dev, nl) if lse is not None else 0, table,
+        ctypes.addressof(desc), _double_bits(softmax_scale),
+        *((_ptr(fn, "workspace", workspace, workspace.dtype, dev), workspace.nbytes)
+          if workspace is not None else (0, 0))))
+
+
+def _double_bits(x: float) -> int:
+    return _q_of(_of_d(x))[0]
+
+
+_of_d, _q_of = struct.Struct("=d").pack, struct.Struct("=q").unpack
 
 
 def seg_attn_tree(q, k_pool, v_pool, out, lse, dev_table, desc, softmax_scale, workspace=None,
@@ -771,16 +809,15 @@ def seg_attn_kv_move(k_pool, v_pool, src, dst, offsets=None, stream=None) -> Non
     dev = _cuda_device(fn, "k_pool", k_pool, 3)
     S, hk, d = k_pool.shape
     kind = k_pool.dtype
-    if kind is not torch.bfloat16 and kind is not torch.uint8:
+    if kind is not _BF16 and kind is not _U8:
         _bad(fn, f"k_pool: bfloat16 or uint8, not {kind}")
     n = src.numel()
-    groups = 0
+    offs = groups = 0
     if offsets is not None:
-        groups = offsets.numel() - 1
+        offs, groups = _ptr(fn, "offsets", offsets, _I32, dev), offsets.numel() - 1
         if groups < 0:
             _bad(fn, "offsets: at least one value")
-    args = (_ptr(fn, "k_pool", k_pool, kind, dev), _ptr(fn, "v_pool", v_pool, kind, dev, S * hk * d),
-            _ptr(fn, "src", src, torch.int32, dev, n), _ptr(fn, "dst", dst, torch.int32, dev, n), n,
-            _ptr(fn, "offsets", offsets, torch.int32, dev) if offsets is not None else None,
-            groups, hk, d, 2 if kind is torch.bfloat16 else 1, S)
-    _invoke(fn, dev, stream, args)
+    _invoke(fn, dev, stream, (
+        _ptr(fn, "k_pool", k_pool, kind, dev), _ptr(fn, "v_pool", v_pool, kind, dev, S * hk * d),
+        _ptr(fn, "src", src, _I32, dev, n), _ptr(fn, "dst", dst, _I32, dev, n), n, offs, groups,
+        hk, d, 2 if kind is _BF16 else 1, S))
