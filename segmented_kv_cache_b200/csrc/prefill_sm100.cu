@@ -8,13 +8,12 @@
 //
 // K/V tiles are 128 consecutive *logical* keys.  Segments (Flood README,
 // "Introduction": contiguous runs in a shared slot pool) make every row's
-// slot known up front, so the producer warp gathers the tile row by row with
-// TMA gather4 (four pool rows per instruction) straight into the 128-byte
-// swizzled layout the tensor cores read; keys past the end of the request
-// are clamped to its last key and masked.  A tile whose 128 keys are 128
-// consecutive pool slots (the common case: segments are long) is instead
-// loaded as two tiled boxes, which the TMA engine moves far faster than 64
-// four-row gathers.
+// slot known up front.  A tile whose 128 keys are 128 consecutive pool slots
+// (the common case: segments are long) is loaded as two tiled boxes straight
+// into the 128-byte swizzled layout the tensor cores read; a tile that
+// straddles segments as boxes of 32 and 8 keys where the slots allow it and
+// TMA gather4 (four pool rows per instruction) where they do not.  Keys past
+// the end of the request are clamped to its last key and masked.
 //
 // Warp roles (two query tiles: 10 warps, 12 over an FP8 cache; one: 6 and 10):
 //   warp 0       TMA producer: Q tiles once, then a K ring and a V ring
@@ -57,6 +56,7 @@
 #include <atomic>
 #include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "ptx_sm100.cuh"
 #include "seg_attn_internal.h"
@@ -93,6 +93,12 @@ std::atomic<uint64_t> g_stall_wait_ns{kWaitLimitNs};
 std::atomic<int> g_order_delay_ns{0};
 constexpr float kRescaleLog2 = 8.0f;
 constexpr uint32_t kHalfBytes = 128 * 128;  // 128 rows x 64 bf16 (one swizzle-128B panel)
+
+// Tensor maps of one pool: single rows (gathered four at a time) and boxes of 8, 32 and
+// 128 consecutive slots of one kv head.
+struct PoolMaps {
+  CUtensorMap row, box8, box32, box128;
+};
 
 struct PrefillParams {
   __nv_bfloat16* out;
@@ -243,9 +249,8 @@ __device__ __forceinline__ bool widen_tile_in_place(uint8_t* slot, int ct, bool 
 // V tile, and the rows that do see such a key get them added at the end.
 template <int D, bool SINGLE, bool FP8, bool TMA_OUT, bool TREE>
 __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
-    prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k3,
-                   const __grid_constant__ CUtensorMap tm_v3, const __grid_constant__ CUtensorMap tm_o,
+    prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
+                   const __grid_constant__ PoolMaps tm_k, const __grid_constant__ PoolMaps tm_v,
                    const PrefillParams p) {
   using namespace ptx;
   constexpr int HALVES = D / 64;
@@ -337,10 +342,8 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
   }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tm_q);
-    prefetch_tensormap(&tm_k);
-    prefetch_tensormap(&tm_v);
-    prefetch_tensormap(&tm_k3);
-    prefetch_tensormap(&tm_v3);
+    prefetch_tensormap(&tm_k.box128);
+    prefetch_tensormap(&tm_v.box128);
     prefetch_tensormap(&tm_o);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -367,75 +370,97 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
         if (k0_early) {
           mbar_expect_tx(k_full, TILE);
           for (int h = 0; h < HALVES; ++h)
-            tma_load_3d(sK + h * kHalfBytes, &tm_k3, k_full, 64 * h, g, w3.x);
+            tma_load_3d(sK + h * kHalfBytes, &tm_k.box128, k_full, 64 * h, g, w3.x);
         }
       }
       int seg = w2.w;
       const int seg_end = w1.w;
       // Pool rows of K tile i: lane l holds logical keys 4l .. 4l + 3 (keys past the
       // request are clamped to its last key).  Most tiles are 128 consecutive pool
-      // slots (segments are long): one tiled box per 64-column half; tiles that
-      // straddle a segment boundary or the end of the request are gathered row by
-      // row.  Tiles are visited in increasing order (the segment cursor only moves on).
+      // slots (segments are long): one tiled box per 64-column half.  In a tile that
+      // straddles a segment boundary or the end of the request, every aligned group of 32
+      // or 8 keys in consecutive slots is a box of its own and only the rest is gathered
+      // four rows at a time (a gather of 4 rows costs the TMA engine as much as a box of
+      // 32: gathering all 128 rows took 2.3 us, 16 copies where there were 64 take 0.6).
+      // Drafted tokens: rows past the request are not loaded (clean_v).  Tiles are
+      // visited in increasing order (the segment cursor only moves on).
+      enum { kNothing = -1, kGather = 0, kBox8 = 1, kBox32 = 2 };
       struct TileRows {
         int rows[4];
-        int slot0;
+        int slot0;   // contiguous: the tile's first slot; otherwise this lane's
+        int kind;    // not contiguous: what this lane loads
+        int count;   // rows loaded
         bool contiguous;
       };
       auto tile_rows = [&](int i, TileRows& tr) {
         // the usual case: all 128 keys inside the segment of the first one, i.e. 128
         // consecutive pool slots -- one lookup, the same on every lane
-        {
-          const int j0 = (kt0 + i) * kTileKeys;
-          while (seg + 1 < seg_end && __ldg(p.tab.seg_kstart + seg + 1) <= j0) ++seg;
-          const int ks = __ldg(p.tab.seg_kstart + seg);
-          if (j0 + kTileKeys <= ks + __ldg(p.tab.seg_len + seg)) {
-            tr.slot0 = __ldg(p.tab.seg_start + seg) + (j0 - ks);
-            tr.contiguous = true;
-            return;
-          }
+        const int j0 = (kt0 + i) * kTileKeys;
+        tr.count = kTileKeys;
+        while (seg + 1 < seg_end && __ldg(p.tab.seg_kstart + seg + 1) <= j0) ++seg;
+        const int ks = __ldg(p.tab.seg_kstart + seg);
+        if (j0 + kTileKeys <= ks + __ldg(p.tab.seg_len + seg)) {
+          tr.slot0 = __ldg(p.tab.seg_start + seg) + (j0 - ks);
+          tr.contiguous = true;
+          return;
         }
-        int slot_first = 0;
-        bool run = true;
+        bool four = true;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = min((kt0 + i) * kTileKeys + 4 * lane + e, k_len - 1);
+          const int j = min(j0 + 4 * lane + e, k_len - 1);
           while (seg + 1 < seg_end && __ldg(p.tab.seg_kstart + seg + 1) <= j) ++seg;
           const int slot = __ldg(p.tab.seg_start + seg) + (j - __ldg(p.tab.seg_kstart + seg));
           tr.rows[e] = slot * p.kv_heads + g;
-          if (e == 0) slot_first = slot;
+          if (e == 0) tr.slot0 = slot;
+          four &= slot == tr.slot0 + e;
         }
-        tr.slot0 = __shfl_sync(0xffffffffu, slot_first, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) run &= tr.rows[e] == (tr.slot0 + 4 * lane + e) * p.kv_heads + g;
-        tr.contiguous = __all_sync(0xffffffffu, run);
-      };
-      auto load_tile = [&](const TileRows& tr, uint8_t* dst, const CUtensorMap* tiled,
-                           const CUtensorMap* rowmap, uint64_t* bar) {
-        if (lane == 0) mbar_expect_tx(bar, TILE);
-        __syncwarp();
+        // lanes whose rows are consecutive slots, and follow those of the lane before
+        const uint32_t runs = __ballot_sync(0xffffffffu, four);
+        const int before = __shfl_up_sync(0xffffffffu, tr.slot0, 1);
+        const uint32_t links = __ballot_sync(0xffffffffu, tr.slot0 == before + 4);
+        tr.contiguous = runs == 0xffffffffu && (links | 1u) == 0xffffffffu;
         if (tr.contiguous) {
-          if (lane == 0)
-            for (int h = 0; h < HALVES; ++h)
-              tma_load_3d(dst + h * kHalfBytes, tiled, bar, 64 * h, g, tr.slot0);
-        } else {
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h)
-            tma_gather4(dst + h * kHalfBytes + lane * 512, rowmap, bar, 64 * h, tr.rows[0],
-                        tr.rows[1], tr.rows[2], tr.rows[3]);
+          tr.slot0 = __shfl_sync(0xffffffffu, tr.slot0, 0);
+          return;
+        }
+        const uint32_t o = runs >> (lane & ~7) & 0xffu, ol = links >> (lane & ~7) & 0xfeu;
+        const uint32_t w = runs >> (lane & ~1) & 3u, wl = links >> (lane & ~1) & 2u;
+        if (o == 0xffu && ol == 0xfeu)
+          tr.kind = (lane & 7) == 0 ? kBox32 : kNothing;
+        else if (w == 3u && wl == 2u)
+          tr.kind = (lane & 1) == 0 ? kBox8 : kNothing;
+        else
+          tr.kind = kGather;
+        if (TREE) {
+          const int left = k_len - j0;
+          if (4 * lane >= left) tr.kind = kNothing;
+          tr.count = min(kTileKeys, (left + 3) & ~3);
         }
       };
-      // FP8: raw code rows (D bytes each), no swizzle
-      auto load_codes = [&](const TileRows& tr, uint8_t* dst, const CUtensorMap* tiled,
-                            const CUtensorMap* rowmap, uint64_t* bar) {
-        if (lane == 0) mbar_expect_tx(bar, kTileKeys * D);
+      // the rows of a tile, `bytes` each, `cols` columns per box and `panels` of them
+      auto load_rows = [&](const TileRows& tr, uint8_t* dst, const PoolMaps& map, uint64_t* bar,
+                           int cols, int panels, int bytes) {
+        if (lane == 0) mbar_expect_tx(bar, tr.count * panels * bytes);
         __syncwarp();
-        if (tr.contiguous) {
-          if (lane == 0) tma_load_3d(dst, tiled, bar, 0, g, tr.slot0);
-        } else {
-          tma_gather4(dst + lane * 4 * D, rowmap, bar, 0, tr.rows[0], tr.rows[1], tr.rows[2],
-                      tr.rows[3]);
+        for (int h = 0; h < panels; ++h) {
+          uint8_t* at = dst + h * kHalfBytes + (tr.contiguous ? 0 : lane * 4 * bytes);
+          if (tr.contiguous) {
+            if (lane == 0) tma_load_3d(at, &map.box128, bar, cols * h, g, tr.slot0);
+          } else if (tr.kind == kBox32) {
+            tma_load_3d(at, &map.box32, bar, cols * h, g, tr.slot0);
+          } else if (tr.kind == kBox8) {
+            tma_load_3d(at, &map.box8, bar, cols * h, g, tr.slot0);
+          } else if (tr.kind == kGather) {
+            tma_gather4(at, &map.row, bar, cols * h, tr.rows[0], tr.rows[1], tr.rows[2], tr.rows[3]);
+          }
         }
+      };
+      // bf16: 64-column panels in the swizzled layout; FP8: raw code rows, no swizzle
+      auto load_tile = [&](const TileRows& tr, uint8_t* dst, const PoolMaps& map, uint64_t* bar) {
+        load_rows(tr, dst, map, bar, 64, HALVES, 128);
+      };
+      auto load_codes = [&](const TileRows& tr, uint8_t* dst, const PoolMaps& map, uint64_t* bar) {
+        load_rows(tr, dst, map, bar, 0, 1, D);
       };
       auto load_k = [&](int i, const TileRows& tr) -> bool {
         // stall test: stop loading here, as a copy that never lands would; the
@@ -446,9 +471,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
                                                wait_limit, true)))
           return false;
         if (FP8)  // codes into the slot's second half, widened there by the last warps
-          load_codes(tr, sK + st * TILE + TILE / 2, &tm_k3, &tm_k, code_k + st);
+          load_codes(tr, sK + st * TILE + TILE / 2, tm_k, code_k + st);
         else
-          load_tile(tr, sK + st * TILE, &tm_k3, &tm_k, k_full + st);
+          load_tile(tr, sK + st * TILE, tm_k, k_full + st);
         ++k_issued;
         return true;
       };
@@ -458,9 +483,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
                                                wait_limit, true)))
           return false;
         if (FP8)
-          load_codes(tr, sV + st * TILE + TILE / 2, &tm_v3, &tm_v, code_v + st);
+          load_codes(tr, sV + st * TILE + TILE / 2, tm_v, code_v + st);
         else
-          load_tile(tr, sV + st * TILE, &tm_v3, &tm_v, v_full + st);
+          load_tile(tr, sV + st * TILE, tm_v, v_full + st);
         ++v_issued;
         return true;
       };
@@ -727,6 +752,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     if (TREE && row_valid)
       mask_row = p.mask_base + ((uint64_t)(uint32_t)w3.y | ((uint64_t)(uint32_t)w3.z << 32)) +
                  (int64_t)qi * ((q_len + 31) >> 5);
+    if (TREE && mask_row) prefetch_global(mask_row);
     // TREE: which of the 32 keys from drafted key `at` on this row sees (at < 0: cached
     // keys, all seen, come first)
     auto mask_word = [&](int at) -> uint32_t {
@@ -899,15 +925,26 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       return __all_sync(0xffffffffu,
                         mbar_wait(o_full + t, (i - 1) & 1, abort_flag, wait_limit)) != 0;
     };
-    // TREE, tile with drafted keys: V row `row` of the tile, when it is a drafted key's (or
-    // past the last key), gets zeros for values that are not finite.  Query tile 0's
+    // TREE, tile with drafted keys: V row `row` of the tile, when it is a drafted key's,
+    // gets zeros for values that are not finite, and is all zeros past the last key.  Query tile 0's
     // threads (dual: the group that has the K tile) do it before they signal P; the PV of
     // query tile 1 is issued after tile 0's.
     auto clean_v = [&](int i) -> bool {
       const int sv = i % RV;
       if (!__all_sync(0xffffffffu, mbar_wait(v_full + sv, (i / RV) & 1, abort_flag, wait_limit)))
         return false;
-      if ((kt0 + i) * kTileKeys + row < prior) return true;
+      const int key = (kt0 + i) * kTileKeys + row;
+      if (key < prior) return true;
+      if (key >= k_len) {  // a row past the request: whatever shared memory held
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(sV + sv * TILE + h * kHalfBytes + row * 128 +
+                                      ((c ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        return true;
+      }
       constexpr uint32_t kExp = FP8 ? 0x7c00u : 0x7f80u;  // f16 (widened) or bf16
       bool found = false;
 #pragma unroll
@@ -1311,16 +1348,14 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
 }
 
 template <int D, bool SINGLE, bool FP8, bool TMA_OUT, bool TREE>
-int launch_items(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                 const CUtensorMap& tk3, const CUtensorMap& tv3, const CUtensorMap& to,
-                 const PrefillParams& p, int n,
-                 cudaStream_t stream) {
+int launch_items(const CUtensorMap& tq, const CUtensorMap& to, const PoolMaps& tk,
+                 const PoolMaps& tv, const PrefillParams& p, int n, cudaStream_t stream) {
   constexpr size_t smem = prefill_smem_bytes<D, SINGLE>();
   if (cudaFuncSetAttribute(prefill_kernel<D, SINGLE, FP8, TMA_OUT, TREE>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SEG_ATTN_ERR_CUDA;
   prefill_kernel<D, SINGLE, FP8, TMA_OUT, TREE>
-      <<<n, cta_threads<SINGLE, FP8>(), smem, stream>>>(tq, tk, tv, tk3, tv3, to, p);
+      <<<n, cta_threads<SINGLE, FP8>(), smem, stream>>>(tq, to, tk, tv, p);
   return cudaGetLastError() == cudaSuccess ? SEG_ATTN_OK : SEG_ATTN_ERR_CUDA;
 }
 
@@ -1328,7 +1363,8 @@ template <int D, bool FP8, bool TREE>
 int launch_prefill_d(const PrefillLaunch& a, cudaStream_t stream) {
   const seg_attn_table_desc& d = *a.desc;
   const int group = d.q_heads / d.kv_heads;
-  CUtensorMap tq, tk, tv, tk3, tv3, to;
+  CUtensorMap tq, to;
+  PoolMaps tk, tv;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)d.q_heads, (cuuint64_t)d.total_q};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)d.q_heads * D * 2};
@@ -1347,17 +1383,21 @@ int launch_prefill_d(const PrefillLaunch& a, cudaStream_t stream) {
     const cuuint64_t dims[2] = {(cuuint64_t)D, empty ? 1ull : (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)D * kElem};
     const cuuint32_t box[2] = {kBoxCols, 1};
-    // with no keys no tile is ever loaded; the query buffer stands in as a valid address
-    if (!encode(&tk, empty ? a.q : a.k_pool, 2, dims, strides, box, FP8)) return SEG_ATTN_ERR_CUDA;
-    if (!encode(&tv, empty ? a.q : a.v_pool, 2, dims, strides, box, FP8)) return SEG_ATTN_ERR_CUDA;
-    // the same pools as [slots][kv heads][d]: 128 consecutive slots of one head per box
+    // the same pools as [slots][kv heads][d]: consecutive slots of one head per box
     const cuuint64_t dims3[3] = {(cuuint64_t)D, (cuuint64_t)d.kv_heads,
                                  empty ? 1ull : (cuuint64_t)d.num_slots};
     const cuuint64_t strides3[2] = {(cuuint64_t)D * kElem, (cuuint64_t)d.kv_heads * D * kElem};
-    const cuuint32_t box3[3] = {kBoxCols, 1, (cuuint32_t)kTileKeys};
-    if (!encode(&tk3, empty ? a.q : a.k_pool, 3, dims3, strides3, box3, FP8))
-      return SEG_ATTN_ERR_CUDA;
-    if (!encode(&tv3, empty ? a.q : a.v_pool, 3, dims3, strides3, box3, FP8))
+    auto pool = [&](PoolMaps& m, const void* base) {
+      if (!encode(&m.row, base, 2, dims, strides, box, FP8)) return false;
+      for (auto [map, slots] : {std::pair<CUtensorMap*, int>{&m.box8, 8}, {&m.box32, 32},
+                                {&m.box128, kTileKeys}}) {
+        const cuuint32_t box3[3] = {kBoxCols, 1, (cuuint32_t)slots};
+        if (!encode(map, base, 3, dims3, strides3, box3, FP8)) return false;
+      }
+      return true;
+    };
+    // with no keys no tile is ever loaded; the query buffer stands in as a valid address
+    if (!pool(tk, empty ? a.q : a.k_pool) || !pool(tv, empty ? a.q : a.v_pool))
       return SEG_ATTN_ERR_CUDA;
   }
   PrefillParams p;
@@ -1390,7 +1430,7 @@ int launch_prefill_d(const PrefillLaunch& a, cudaStream_t stream) {
   auto launch = [&](auto single_tag, auto tma_tag, int base, int n) {
     p.work_base = base;
     return launch_items<D, decltype(single_tag)::value, FP8, decltype(tma_tag)::value || TREE, TREE>(
-        tq, tk, tv, tk3, tv3, to, p, n, stream);
+        tq, to, tk, tv, p, n, stream);
   };
   using T = std::true_type;
   using F = std::false_type;
