@@ -41,8 +41,8 @@
 // One query tile: S double-buffered, each buffer with a P region of its own, so
 // the QK that refills an S buffer never overwrites what the PV before it reads.
 // TMEM columns: O [0,128) P0 [128,192) P1 [192,256) S0 [256,384) S1 [384,512).
-// Over an FP8 cache more warps (two; four with one query tile) widen the E4M3 codes
-// to f16 in place, inside the ring slot whose second half the codes were loaded into.
+// Over an FP8 cache the last two warps widen the E4M3 codes to f16 in place, inside
+// the ring slot whose second half the codes were loaded into.
 // (A single staging tile per K and V, as the one-tile kernel had, exposed every tile's
 // load latency: 64 trees of 16 over 4k keys, 308 us against 87 us of cache reads.)
 // Every mbarrier wait is bounded (1 s); a timeout stops all roles of the CTA,
@@ -68,20 +68,16 @@ __device__ int g_device_error;  // non-zero once a bounded wait gave up
 namespace {
 
 // Warps: producer, MMA issuer, four softmax warps per query tile, and over an FP8 cache
-// the warps that widen E4M3 codes (two with two query tiles, four with one, whose K
-// tiles come twice as fast).  Registers are dealt out per SM sub-partition: 6 warps
-// leave the one-tile bf16 kernel 255 per thread (no spills), 9 to 12 warps 168.
+// one warp that widens the E4M3 codes of K tiles and one for V tiles.  Registers are dealt
+// out per SM sub-partition: 6 or 8 warps leave the one-tile kernels 255 per thread (no
+// spills), 9 to 12 warps 168.
 template <bool SINGLE>
 constexpr int conv_warp0() {
   return SINGLE ? 6 : 10;
 }
-template <bool SINGLE>
-constexpr int conv_threads() {
-  return SINGLE ? 128 : 64;
-}
 template <bool SINGLE, bool FP8>
 constexpr int cta_threads() {
-  return conv_warp0<SINGLE>() * 32 + (FP8 ? conv_threads<SINGLE>() : 0);
+  return (conv_warp0<SINGLE>() + (FP8 ? 2 : 0)) * 32;
 }
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // default limit of a bounded wait
 // Stall test (off by default): the K tile at which every later prefill CTA's
@@ -195,42 +191,46 @@ __device__ __forceinline__ void bf16x8_to_f16x8(uint4& v) {
 // bytes, plain row-major) -> f16 over the whole slot in the 128-byte-swizzled K-major
 // layout the tensor cores read (the layout a tiled TMA load of a bf16 tile produces):
 // row r, 16-byte chunk c of 64-column half h lands at h * kHalfBytes + r * 128 +
-// ((c ^ (r & 7)) * 16).  Thread ct of the NT widening threads owns one 16-code column j
-// of rows r0, r0 + step, ... with step a multiple of 8, so the swizzle phase r & 7 and
-// both store offsets are fixed per thread and the unrolled loop needs no address
-// arithmetic.  The eight lanes of a row group hold columns of both halves, whose chunks
-// share banks: the second half's lanes take the neighbouring row (r0 ^ 1), which turns
-// their even chunks into odd ones, so loads and stores are both free of conflicts.
-// A row's f16 output overwrites code bytes that other threads read, so every thread
-// first loads all of its codes, the NT threads meet at named barrier 1, and only then
-// write.  `landed`: this thread saw the copy complete; the barrier makes it the AND of all
-// threads (what was loaded counts only then), which is returned.
-template <int D, int NT>
-__device__ __forceinline__ bool widen_tile_in_place(uint8_t* slot, int ct, bool landed) {
-  constexpr int kCols = D / 16;
-  constexpr int kRowStep = NT / kCols;
-  constexpr int kRows = kTileKeys / kRowStep;
-  static_assert(kRowStep % 8 == 0, "rows of one thread must share the swizzle phase");
-  const int j = ct % kCols, r0 = (ct / kCols) ^ (j >> 2);
+// ((c ^ (r & 7)) * 16).  One warp walks the tile in passes of 8 rows; a lane has one
+// 16-code column j of row r0 (and, d = 128, r0 + 4), so its offsets are those of the
+// first pass plus a constant.  In place needs no barrier across warps: with d = 128 a
+// row's codes lie exactly under its own second half; with d = 64 the output of row r
+// covers the codes of rows 2 r - 128 and 2 r - 127, never later than r; so it is enough
+// that the warp has loaded a pass before it stores that pass.  The eight lanes of a row
+// (d = 128) hold columns of both halves, whose chunks share banks: the second half's
+// lanes take the neighbouring row (r0 ^ 1), which turns their even chunks into odd ones,
+// so loads and stores are both free of conflicts.
+// One warp per K and per V tile instead of 64 threads per tile with two barriers: the
+// chain of waits, barriers and latencies (1200 cycles a tile, K and V in turn) bounded
+// both kernels.
+template <int D>
+__device__ __forceinline__ void widen_tile(uint8_t* slot, int lane) {
+  constexpr int kCols = D / 16;             // 16-code columns of a row
+  constexpr int kRowStep = 32 / kCols;      // rows of one load: 4 (d = 128) or 8 (d = 64)
+  constexpr int kBatch = 32 / kRowStep;     // loads in flight per thread: 32 rows
+  const int j = lane % kCols, r0 = (lane / kCols) ^ (j >> 2);
+  const int c0 = (j & 3) * 2;
   const uint8_t* s = slot + (D / 64) * kHalfBytes / 2 + r0 * D + 16 * j;
-  uint4 w[kRows];
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) w[k] = *reinterpret_cast<const uint4*>(s + k * kRowStep * D);
-  if (!ptx::named_barrier_and(1, NT, landed)) return false;
-  const int sw = r0 & 7, c0 = (j & 3) * 2;
   uint8_t* d = slot + (j >> 2) * kHalfBytes + r0 * 128;
-  const int o0 = (c0 ^ sw) << 4, o1 = ((c0 + 1) ^ sw) << 4;
+#pragma unroll 1
+  for (int r = 0; r < kTileKeys; r += 32, s += 32 * D, d += 32 * 128) {
+    uint4 w[kBatch];
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    uint4 lo, hi;
-    ptx::e4m3x4_to_f16x4(w[k].x, lo.x, lo.y);
-    ptx::e4m3x4_to_f16x4(w[k].y, lo.z, lo.w);
-    ptx::e4m3x4_to_f16x4(w[k].z, hi.x, hi.y);
-    ptx::e4m3x4_to_f16x4(w[k].w, hi.z, hi.w);
-    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o0) = lo;
-    *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + o1) = hi;
+    for (int k = 0; k < kBatch; ++k)
+      w[k] = *reinterpret_cast<const uint4*>(s + k * kRowStep * D);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int sw = (r0 + k * kRowStep) & 7;
+      uint4 lo, hi;
+      ptx::e4m3x4_to_f16x4(w[k].x, lo.x, lo.y);
+      ptx::e4m3x4_to_f16x4(w[k].y, lo.z, lo.w);
+      ptx::e4m3x4_to_f16x4(w[k].z, hi.x, hi.y);
+      ptx::e4m3x4_to_f16x4(w[k].w, hi.z, hi.w);
+      *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + ((c0 ^ sw) << 4)) = lo;
+      *reinterpret_cast<uint4*>(d + k * kRowStep * 128 + (((c0 + 1) ^ sw) << 4)) = hi;
+    }
   }
-  return true;
 }
 
 // SINGLE: every item of the launch has queries in its first query tile only
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   constexpr int RK = kRingK, RV = ring_v<SINGLE>();
-  constexpr int kConvWarp0 = conv_warp0<SINGLE>(), kConvThreads = conv_threads<SINGLE>();
+  constexpr int kConvWarp0 = conv_warp0<SINGLE>();
   // Q tiles at sQ + t * TILE.  Two query tiles (QT): P_t in tensor memory columns
   // [384 + 64 t, 448 + 64 t).
   constexpr bool QT = !SINGLE;
@@ -314,13 +314,13 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    // FP8: the rings are filled by the converter threads, not by TMA
+    // full: the copy's bytes, or over an FP8 cache the widening warp's arrival
     for (int s = 0; s < RK; ++s) {
-      mbar_init(k_full + s, FP8 ? kConvThreads : 1);
+      mbar_init(k_full + s, 1);
       mbar_init(k_empty + s, 1);
     }
     for (int s = 0; s < RV; ++s) {
-      mbar_init(v_full + s, FP8 ? kConvThreads : 1);
+      mbar_init(v_full + s, 1);
       mbar_init(v_empty + s, 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -716,27 +716,21 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     // ------------------------------------------------------------ FP8 code widening
     // E4M3 tile -> f16 K (V) ring slot, then make the generic-proxy writes
     // visible to the tensor cores before signalling the ring slot full.
-    const int ct = threadIdx.x - kConvWarp0 * 32;
-    bool ok = true;
-    // codes in the slot's second half, in the producer's order.  The widening threads agree on every wait's outcome at
-    // the barrier of the widening (all or none go on).
-    auto widen = [&](uint8_t* slot, uint64_t* landed, uint32_t parity, uint64_t* full) -> bool {
-      const bool got = mbar_try_wait(smem_u32(landed), parity) ||
-                       mbar_wait(landed, parity, abort_flag, wait_limit);
-      if (!widen_tile_in_place<D, kConvThreads>(slot, ct, got)) return false;
+    const bool is_k = warp == kConvWarp0;
+    uint8_t* ring = is_k ? sK : sV;
+    uint64_t* landed = is_k ? code_k : code_v;
+    uint64_t* full = is_k ? k_full : v_full;
+    const int depth = is_k ? RK : RV;
+    for (int i = 0, st = 0, ph = 0; i < n_tiles; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(landed + st, ph, abort_flag, wait_limit))) break;
+      widen_tile<D>(ring + st * TILE, lane);
       fence_proxy_async_smem();
-      mbar_arrive(full);
-      return true;
-    };
-    for (int i = 0; ok && i < ahead && i < n_tiles; ++i)
-      ok = widen(sK + i * TILE, code_k + i, 0, k_full + i);
-    for (int i = 0; ok && i < n_tiles; ++i) {
-      if (i + ahead < n_tiles) {
-        const int nk = i + ahead, sk = nk % RK;
-        if (!(ok = widen(sK + sk * TILE, code_k + sk, (nk / RK) & 1, k_full + sk))) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + st);
+      if (++st == depth) {
+        st = 0;
+        ph ^= 1;
       }
-      const int sv = i % RV;
-      ok = widen(sV + sv * TILE, code_v + sv, (i / RV) & 1, v_full + sv);
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
