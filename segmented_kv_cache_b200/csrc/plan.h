@@ -62,10 +62,11 @@ struct Pieces {
   int32_t single = 0;           // single-tile pieces (the tail of `work`)
 };
 
-// Cut items into pieces and order them (comment at the definition).
-// `min_piece`: the shortest K range of a piece of a split item, in K tiles.
+// Cut items into pieces and order them (comments at the definitions).
 void plan_pieces(const std::vector<PItem>& items, int max_split, std::vector<Row4>& citems,
-                 Pieces& out, int min_piece = kMinPieceTiles);
+                 Pieces& out);
+void emit_pieces(const std::vector<PItem>& items, const std::vector<std::vector<int32_t>>& ends,
+                 std::vector<Row4>& citems, Pieces& out);
 
 // Fill the per-request words of each piece (comment at the definition).
 void fill_request_words(std::vector<Row16>& work, const std::vector<int32_t>& q_off,

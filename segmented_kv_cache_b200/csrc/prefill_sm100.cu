@@ -742,21 +742,25 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     const int head = g * p.group + row % p.group;
     const bool row_valid = qi < q_len;
     const int prior = k_len - q_len;  // TREE: keys before the drafted ones
-    const uint32_t* mask_row = nullptr;
-    if (TREE && row_valid)
-      mask_row = p.mask_base + ((uint64_t)(uint32_t)w3.y | ((uint64_t)(uint32_t)w3.z << 32)) +
-                 (int64_t)qi * ((q_len + 31) >> 5);
-    if (TREE && mask_row) prefetch_global(mask_row);
+    // TREE: this row's mask row.  Read anew where it is needed (the work row's words
+    // through a volatile access): kept in registers across the K tiles it would cost spills.
+    auto mask_row = [&]() -> const uint32_t* {
+      const volatile uint32_t* w =
+          reinterpret_cast<const volatile uint32_t*>(p.tab.work + 4 * (p.work_base + blockIdx.x) + 3);
+      const uint64_t at = (uint64_t)w[1] | ((uint64_t)w[2] << 32);
+      return p.mask_base + at + (int64_t)qi * ((q_len + 31) >> 5);
+    };
+    if (TREE && row_valid) prefetch_global(mask_row());
     // TREE: which of the 32 keys from drafted key `at` on this row sees (at < 0: cached
     // keys, all seen, come first)
-    auto mask_word = [&](int at) -> uint32_t {
+    auto mask_word = [&](const uint32_t* mrow, int at) -> uint32_t {
       if (at <= -32) return 0xffffffffu;
-      if (!mask_row) return 0u;
+      if (!row_valid) return 0u;
       const int words = (q_len + 31) >> 5;
-      if (at < 0) return (__ldg(mask_row) << -at) | ((1u << -at) - 1u);
+      if (at < 0) return (__ldg(mrow) << -at) | ((1u << -at) - 1u);
       const int w = at >> 5;
-      const uint32_t lo = w < words ? __ldg(mask_row + w) : 0u;
-      const uint32_t hi = w + 1 < words ? __ldg(mask_row + w + 1) : 0u;
+      const uint32_t lo = w < words ? __ldg(mrow + w) : 0u;
+      const uint32_t hi = w + 1 < words ? __ldg(mrow + w + 1) : 0u;
       return __funnelshift_r(lo, hi, at & 31);
     };
     const int vis = TREE ? prior : p.causal ? min(k_len, k_len - q_len + qi + 1) : k_len;
@@ -783,9 +787,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, wait_limit));
       if (ok) {
         if (!dual || t == 0) {
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < HALVES; ++h)
-#pragma unroll
+#pragma unroll 4
             for (int c = 0; c < 8; ++c) {
               uint4* chunk = reinterpret_cast<uint4*>(sQ + t * QSTRIDE + h * kHalfBytes +
                                                       row * 128 + ((c ^ (row & 7)) << 4));
@@ -817,9 +821,10 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       }
       if (masked) {
         const int kb = (kt0 + i) * kTileKeys;
+        const uint32_t* mrow = TREE ? mask_row() : nullptr;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint32_t word = TREE ? mask_word(kb + 32 * c - prior) : 0u;
+          const uint32_t word = TREE ? mask_word(mrow, kb + 32 * c - prior) : 0u;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const bool hide = TREE ? !((word >> e) & 1u) : kb + 32 * c + e >= vis;
@@ -893,7 +898,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
             !__all_sync(0xffffffffu, mbar_wait(o_full + t, (j - 1) & 1, abort_flag, wait_limit)))
           return false;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * c, o);
@@ -930,9 +935,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       const int key = (kt0 + i) * kTileKeys + row;
       if (key < prior) return true;
       if (key >= k_len) {  // a row past the request: whatever shared memory held
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < HALVES; ++h)
-#pragma unroll
+#pragma unroll 2
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<uint4*>(sV + sv * TILE + h * kHalfBytes + row * 128 +
                                       ((c ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -941,9 +946,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       }
       constexpr uint32_t kExp = FP8 ? 0x7c00u : 0x7f80u;  // f16 (widened) or bf16
       bool found = false;
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < HALVES; ++h)
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < 8; ++c) {
           uint32_t* w = reinterpret_cast<uint32_t*>(sV + sv * TILE + h * kHalfBytes + row * 128 +
                                                     ((c ^ (row & 7)) << 4));
@@ -1017,6 +1022,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     // to O in tensor memory, as its product with a positive weight would be (a NaN or an
     // infinity).  32 columns at a time, every lane of the warp in step.
     auto add_nonfinite = [&]() {
+      const uint32_t* mrow = mask_row();
       const int first = max(kt0 * kTileKeys - prior, 0);
       const int last = min((kt0 + n_tiles) * kTileKeys - prior, q_len);
 #pragma unroll 1
@@ -1028,7 +1034,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
         for (int j = first; j < last; ++j) {
           // dual: drafted keys in this group's K tiles
           if (dual && ((((prior + j) / kTileKeys) ^ kt0 ^ t) & 1)) continue;
-          const bool seen = mask_word(j) & 1u;
+          const bool seen = mask_word(mrow, j) & 1u;
           const int64_t at =
               ((int64_t)__ldg(p.draft_slot + tok0 + j) * p.kv_heads + g) * D + 32 * c;
 #pragma unroll
@@ -1047,42 +1053,44 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       }
       tmem_wait_st();
     };
-    // dual: weight of this group's O and of the other group's, whose O waits in shared
-    // memory (in the K ring, which is free then) as [16-byte chunk][row]
+    // dual: weights of the two groups' O, which group 0 adds up; group 1's (m, l) wait in
+    // shared memory (in the K ring, which is free then)
     float w_own = 1.f, w_other = 0.f;
-    float4* other_o = reinterpret_cast<float4*>(sK);
-    float2* other_ml = reinterpret_cast<float2*>(sK + 128 * D * 4);
-    static_assert(!TREE || 128 * D * 4 + 128 * 8 <= RK * TILE, "exchange fits the K ring");
-    // this row's O (fp32, D columns) in registers: every load issued, one wait
-    auto load_o = [&](uint32_t (&o)[D / 32][32]) {
-      if (n_tiles > 0) {
-        tc_fence_after();
-        if (TREE && *reinterpret_cast<volatile int*>(nonfinite) != 0) add_nonfinite();
-        if constexpr (D == 128) {
-          tmem_ld128(tO, o);
-        } else {
+    float2* other_ml = reinterpret_cast<float2*>(sK);
+    // 32 columns of this row's O (fp32).  The epilogues below walk them in rolled loops: a
+    // CTA runs them once, so their instructions come from the second-level cache at best,
+    // and under a full memory load the unrolled form spent 4 to 10 us on fetching itself.
+    auto load_o = [&](int c, uint32_t (&o)[32]) {
+      if (n_tiles == 0) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + 32 * c, o[c]);
-        }
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) tmem_wait_ld(o[c]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[c][e] = 0u;
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+        return;
       }
-      if (TREE && w_other != 0.f) {
+      tmem_ld32(tO + 32 * c, o);
+      tmem_wait_ld(o);
+      // the other group's rows lie in the same tensor-memory lanes, 128 columns on
+      if (TREE && __any_sync(0xffffffffu, w_other != 0.f)) {
+        uint32_t x[32];
+        tmem_ld32(lane_base + 128 + 32 * c, x);
+        tmem_wait_ld(x);
 #pragma unroll
-        for (int c = 0; c < D / 4; ++c) {
-          const float4 x = other_o[c * 128 + row];
-          uint32_t* y = &o[c / 8][4 * (c % 8)];
-          y[0] = __float_as_uint(__uint_as_float(y[0]) * w_own + x.x * w_other);
-          y[1] = __float_as_uint(__uint_as_float(y[1]) * w_own + x.y * w_other);
-          y[2] = __float_as_uint(__uint_as_float(y[2]) * w_own + x.z * w_other);
-          y[3] = __float_as_uint(__uint_as_float(y[3]) * w_own + x.w * w_other);
+        for (int e = 0; e < 32; ++e) {
+          float y = __uint_as_float(o[e]) * w_own;
+          if (w_other != 0.f) y = fmaf(__uint_as_float(x[e]), w_other, y);
+          o[e] = __float_as_uint(y);
         }
       }
+    };
+    // before the first load_o
+    auto open_o = [&]() {
+      tc_fence_after();
+      if (TREE && n_tiles > 0 && *reinterpret_cast<volatile int*>(nonfinite) != 0) add_nonfinite();
+    };
+    // 16-byte chunk k (eight columns) of 32 loaded ones, scaled, as bf16
+    auto pack_o = [&](const uint32_t (&o)[32], int k, float inv) {
+      auto f = [&](int e) { return __uint_as_float(o[8 * k + e]) * inv; };
+      return make_uint4(pack_bf16(f(0), f(1)), pack_bf16(f(2), f(3)), pack_bf16(f(4), f(5)),
+                        pack_bf16(f(6), f(7)));
     };
     // PV complete up to tile n - 2 (two tiles: P(n - 1) was written after it; one
     // tile: confirmed before P(n - 1) was signalled), so o_full is at completion
@@ -1091,23 +1099,20 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       ok = __all_sync(0xffffffffu,
                       mbar_wait(o_full + t, (my_tiles - 1) & 1, abort_flag, wait_limit));
     if (dual) {
-      // Group 1 hands its state over and is done.  All of the item's QK are complete once
-      // its last PV is (QK of the last K tile is issued before it), so the K ring is free.
-      // Both groups meet at an AND of their outcomes, so a give-up leaves no one waiting.
+      // Group 1 hands over its (m, l) and is done; its O stays in tensor memory, complete.
+      // All of the item's QK are complete once its last PV is (QK of the last K tile is
+      // issued before it), so the K ring is free.  Both groups meet at an AND of their
+      // outcomes, so a give-up leaves no one waiting.
       if (t == 1 && ok && my_tiles > 0) {
-        if (warp_live) {
-          uint32_t o[D / 32][32];
-          load_o(o);
-#pragma unroll
-          for (int c = 0; c < D / 4; ++c) {
-            const uint32_t* y = &o[c / 8][4 * (c % 8)];
-            other_o[c * 128 + row] = make_float4(__uint_as_float(y[0]), __uint_as_float(y[1]),
-                                                 __uint_as_float(y[2]), __uint_as_float(y[3]));
-          }
+        if (*reinterpret_cast<volatile int*>(nonfinite) != 0) {
+          tc_fence_after();
+          add_nonfinite();
         }
         other_ml[row] = make_float2(m_ref, l);
+        tc_fence_before();
       }
       ok = named_barrier_and(4, 256, ok);
+      tc_fence_after();
       if (t == 1) ok = false;  // nothing to write
       if (ok && n_tiles > 1) {
         const float2 ml = other_ml[row];
@@ -1123,42 +1128,35 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     // Results leave through shared memory so that whole rows are stored: a thread
     // owns one row, and its own 16-byte pieces of it would put every warp store on 32
     // different lines.  The tile's query region is free (the commit of the tile's
-    // last PV covers every earlier MMA).  Partials of a split piece: each warp stages
-    // its 32 rows in a quarter of it, 16-byte chunk c of row-local r at
-    // ((c & ~7) | ((c ^ r) & 7)), and copies rows out with consecutive lanes on
-    // consecutive chunks.
+    // last PV covers every earlier MMA).  Each warp stages its 32 rows in a quarter of it
+    // and copies rows out with consecutive lanes on consecutive 16-byte chunks; chunk c of
+    // row-local r sits at ((c & ~7) | ((c ^ r) & 7)).
     uint8_t* stage_w = sQ + t * QSTRIDE + quad * (QSTRIDE / 4);
     auto swz = [](int c, int r) { return (c & ~7) | ((c ^ r) & 7); };
     if (ok && slot >= 0) {
       // piece of a split item (or of a shared-prefix pass): O / l and log2(sum of exp)
-      // of this key range, for every row that holds a query; fp32 rows go out in
-      // passes of PCOLS columns (the staging quarter holds 32 rows of PCOLS floats)
-      constexpr int PCOLS = (int)(QSTRIDE / 512) < D ? (int)(QSTRIDE / 512) : D;
-      constexpr int PCH = PCOLS / 4;        // 16-byte chunks per row per pass
-      constexpr int RPI = 32 / PCH;         // rows per warp instruction of the copy
+      // of this key range, for every row that holds a query; fp32 rows go out in passes
+      // of 32 columns
       const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
       const int64_t prow0 = (int64_t)slot * kItemRows + t * kTileRows + quad * 32;
-      uint32_t o[D / 32][32];
-      load_o(o);
+      open_o();
+#pragma unroll 1
+      for (int pass = 0; pass < D / 32; ++pass) {
+        uint32_t o[32];
+        load_o(pass, o);
 #pragma unroll
-      for (int pass = 0; pass < D / PCOLS; ++pass) {
-#pragma unroll
-        for (int c = 0; c < PCH; ++c) {
-          const int col = pass * PCOLS + 4 * c;
-          const float4 v = make_float4(__uint_as_float(o[col / 32][col % 32]) * inv,
-                                       __uint_as_float(o[col / 32][col % 32 + 1]) * inv,
-                                       __uint_as_float(o[col / 32][col % 32 + 2]) * inv,
-                                       __uint_as_float(o[col / 32][col % 32 + 3]) * inv);
-          *reinterpret_cast<float4*>(stage_w + lane * (PCOLS * 4) + swz(c, lane) * 16) = v;
-        }
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<float4*>(stage_w + lane * 128 + swz(c, lane) * 16) =
+              make_float4(__uint_as_float(o[4 * c]) * inv, __uint_as_float(o[4 * c + 1]) * inv,
+                          __uint_as_float(o[4 * c + 2]) * inv, __uint_as_float(o[4 * c + 3]) * inv);
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 32; k += RPI) {
-          const int lr = k + lane / PCH, c = lane % PCH;
-          const int qi_r = q0 + t * p.qpt + (quad * 32 + lr) / p.group;
+#pragma unroll 4
+        for (int k = 0; k < 32; k += 4) {
+          const int lr = k + lane / 8, c = lane % 8;
+          const int qi_r = q0 + tq * p.qpt + (quad * 32 + lr) / p.group;
           if (qi_r < q_len)
-            *reinterpret_cast<float4*>(p.part_o + (prow0 + lr) * D + pass * PCOLS + 4 * c) =
-                *reinterpret_cast<const float4*>(stage_w + lr * (PCOLS * 4) + swz(c, lr) * 16);
+            *reinterpret_cast<float4*>(p.part_o + (prow0 + lr) * D + pass * 32 + 4 * c) =
+                *reinterpret_cast<const float4*>(stage_w + lr * 128 + swz(c, lr) * 16);
         }
         __syncwarp();
       }
@@ -1168,22 +1166,18 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       constexpr int CH = D / 8;    // 16-byte chunks of a bf16 row
       constexpr int RPI = 32 / CH; // rows per warp instruction of the copy
       const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
-      uint32_t o[D / 32][32];
-      load_o(o);
-#pragma unroll
+      open_o();
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        load_o(c, o);
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint4 v;
-          v.x = pack_bf16(__uint_as_float(o[c][e]) * inv, __uint_as_float(o[c][e + 1]) * inv);
-          v.y = pack_bf16(__uint_as_float(o[c][e + 2]) * inv, __uint_as_float(o[c][e + 3]) * inv);
-          v.z = pack_bf16(__uint_as_float(o[c][e + 4]) * inv, __uint_as_float(o[c][e + 5]) * inv);
-          v.w = pack_bf16(__uint_as_float(o[c][e + 6]) * inv, __uint_as_float(o[c][e + 7]) * inv);
-          *reinterpret_cast<uint4*>(stage_w + lane * (D * 2) + swz((32 * c + e) / 8, lane) * 16) = v;
-        }
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(stage_w + lane * (D * 2) + swz(4 * c + k, lane) * 16) =
+              pack_o(o, k, inv);
       }
       __syncwarp();
-#pragma unroll
+#pragma unroll 4
       for (int k = 0; k < 32; k += RPI) {
         const int lr = k + lane / CH, c = lane % CH;
         const int rr = quad * 32 + lr;
@@ -1213,20 +1207,16 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       const bool go = full ? named_barrier_and(2 + t, 128, ok) : ok;
       if (go) {
         const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
-        uint32_t o[D / 32][32];
-        load_o(o);
-#pragma unroll
+        open_o();
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          load_o(c, o);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 v;
-            v.x = pack_bf16(__uint_as_float(o[c][e]) * inv, __uint_as_float(o[c][e + 1]) * inv);
-            v.y = pack_bf16(__uint_as_float(o[c][e + 2]) * inv, __uint_as_float(o[c][e + 3]) * inv);
-            v.z = pack_bf16(__uint_as_float(o[c][e + 4]) * inv, __uint_as_float(o[c][e + 5]) * inv);
-            v.w = pack_bf16(__uint_as_float(o[c][e + 6]) * inv, __uint_as_float(o[c][e + 7]) * inv);
-            const int ch = (32 * c + e) / 8;  // logical 16-byte chunk of the row
+          for (int k = 0; k < 4; ++k) {
+            const int ch = 4 * c + k;  // logical 16-byte chunk of the row
             *reinterpret_cast<uint4*>(stage_t + (ch >> 3) * kHalfBytes + row * 128 +
-                                      (((ch & 7) ^ (row & 7)) << 4)) = v;
+                                      (((ch & 7) ^ (row & 7)) << 4)) = pack_o(o, k, inv);
           }
         }
         if (full) {
@@ -1242,7 +1232,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
           }
         } else {
           __syncwarp();
-#pragma unroll
+#pragma unroll 4
           for (int k = 0; k < 32; k += RPI) {
             const int rr = quad * 32 + k + lane / CH, c = lane % CH;
             const int qi_r = q0 + t * p.qpt + rr / p.group;

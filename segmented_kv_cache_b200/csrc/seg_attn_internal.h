@@ -17,7 +17,6 @@ constexpr int kMinPieceTiles = 8;       // shortest K range a split prefill piec
 constexpr int kPieceOverheadTiles = 3;  // per-piece cost (prologue, epilogue) in K tiles (traced: ~12 k cycles)
 constexpr int kMaxSplit = 4;            // most pieces one prefill item is cut into
 constexpr int kMaxGroupSplit = 32;      // the same for a pass over a shared prefix
-constexpr int kTreeMinPieceTiles = 1;   // the shortest K range of a piece of drafted tokens
 constexpr int kMinSharedKeys = 256;     // shortest prefix worth a pass of its own
 // decode: key chunks are halved (down to 256 keys) until the grid has this many
 // CTAs -- 4 waves at 2 CTAs per SM, so the last wave's tail stays short

@@ -59,10 +59,10 @@ Segs cut(const Segs& s, int64_t from, int64_t count) {
 // block scheduler does with a grid in that order) and the split factor with the
 // shortest makespan wins (ties keep fewer splits).
 void plan_pieces(const std::vector<PItem>& items, int max_split, std::vector<Row4>& citems,
-                 Pieces& out, int min_piece) {
-  auto pieces_of = [min_piece](int32_t tiles, int f) {
-    if (f <= 1 || tiles < 2 * min_piece) return 1;
-    return std::min(f, tiles / min_piece);
+                 Pieces& out) {
+  auto pieces_of = [](int32_t tiles, int f) {
+    if (f <= 1 || tiles < 2 * kMinPieceTiles) return 1;
+    return std::min(f, tiles / kMinPieceTiles);
   };
   // Longest-first schedule of the pieces on the SMs (each piece costed at its K tiles
   // plus the per-piece start-up and epilogue), for a piece count per item.
@@ -105,12 +105,12 @@ void plan_pieces(const std::vector<PItem>& items, int max_split, std::vector<Row
     std::vector<int> c(items.size());
     for (size_t i = 0; i < items.size(); ++i) {
       const int32_t t = items[i].tiles;
-      if (t < 2 * min_piece) {
+      if (t < 2 * kMinPieceTiles) {
         c[i] = 1;
         continue;
       }
       const int want = (int)std::lround((double)t / len);
-      c[i] = std::max(1, std::min({want, max_split, (int)(t / min_piece)}));
+      c[i] = std::max(1, std::min({want, max_split, (int)(t / kMinPieceTiles)}));
     }
     cands.push_back(std::move(c));
   }
@@ -128,7 +128,17 @@ void plan_pieces(const std::vector<PItem>& items, int max_split, std::vector<Row
         (npieces[j] == npieces[pick] && spans[j] < spans[pick]))
       pick = j;
   }
-  const std::vector<int>& counts = cands[pick];
+  std::vector<std::vector<int32_t>> ends(items.size());
+  for (size_t i = 0; i < items.size(); ++i)
+    for (int j = 1; j <= cands[pick][i]; ++j)
+      ends[i].push_back((int32_t)((int64_t)items[i].tiles * j / cands[pick][i]));
+  emit_pieces(items, ends, citems, out);
+}
+
+// Work rows, partial slots and merge rows of items cut at the given K tiles (each list
+// ascending, its last entry the item's K tiles), in launch order.
+void emit_pieces(const std::vector<PItem>& items, const std::vector<std::vector<int32_t>>& ends,
+                 std::vector<Row4>& citems, Pieces& out) {
   // The one-tile kernel runs a pass only when every item of it is single-tile: a
   // second launch for a few single-tile items would serialise behind the first
   // launch's tail (those items then run two-tile, their empty tile's softmax skipped).
@@ -138,7 +148,7 @@ void plan_pieces(const std::vector<PItem>& items, int max_split, std::vector<Row
   for (size_t i = 0; i < items.size(); ++i) {
     PItem it = items[i];
     it.single = all_single;
-    const int p = counts[i];
+    const int p = (int)ends[i].size();
     const bool slotted = p > 1 || it.cascade;
     const int32_t slot0 = slotted ? out.slots : -1;
     if (slotted) out.slots += p;
@@ -149,8 +159,7 @@ void plan_pieces(const std::vector<PItem>& items, int max_split, std::vector<Row
       out.merge.push_back({it.r, it.g, it.q0, slot0, p, 0, 0, 0});
     }
     for (int j = 0; j < p; ++j) {
-      const int32_t kt0 = (int32_t)((int64_t)it.tiles * j / p);
-      const int32_t kt1 = (int32_t)((int64_t)it.tiles * (j + 1) / p);
+      const int32_t kt0 = j > 0 ? ends[i][j - 1] : 0, kt1 = ends[i][j];
       out.work.push_back({it.r, it.g, it.q0, kt0, kt1, slotted ? slot0 + j : -1,
                           it.single ? 1 : 0, 0, 0, 0, 0, 0, -1, 0, 0, 0});
       out.single += it.single ? 1 : 0;

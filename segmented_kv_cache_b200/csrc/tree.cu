@@ -42,6 +42,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams p) {
   const int tok0 = __ldg(p.tab.q_offsets + req);
   const int q_len = __ldg(p.tab.q_offsets + req + 1) - tok0;
   const int lane = threadIdx.x & 31, gi = lane >> 3, l8 = lane & 7;
+  // launched as a programmatic dependent of the prefill pass: what precedes this line
+  // overlaps its end, what follows reads the partials
+  ptx::grid_dependency_wait();
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int qi = q0 + (row / kTileRows) * p.qpt + (row % kTileRows) / p.group;
   if (qi >= q_len) return;
@@ -156,11 +159,18 @@ int tree(const void* q, const void* k_pool, const void* v_pool, const float* k_s
   // no item has rows past the first tile when every draft fits in it
   const dim3 grid(pass.num_merge,
                   (desc->max_draft <= pass.queries_per_tile ? kTileRows : kItemRows) / 8);
-  if (pass.head_dim == 128)
-    tree_merge_kernel<128><<<grid, 256, 0, st>>>(m);
-  else
-    tree_merge_kernel<64><<<grid, 256, 0, st>>>(m);
-  return cudaGetLastError() == cudaSuccess ? SEG_ATTN_OK : SEG_ATTN_ERR_CUDA;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  const cudaError_t e = pass.head_dim == 128 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<128>, m)
+                                             : cudaLaunchKernelEx(&cfg, tree_merge_kernel<64>, m);
+  return e == cudaSuccess ? SEG_ATTN_OK : SEG_ATTN_ERR_CUDA;
 }
 
 }  // namespace

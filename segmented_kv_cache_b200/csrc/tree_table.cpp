@@ -2,14 +2,15 @@
 //
 // The table is that of a prefill without a causal mask, whose work rows also say
 // where the request's mask rows begin; the K tiles that reach past the cached keys
-// look at them.  Few items are cut finely along the keys (down to
-// kTreeMinPieceTiles tiles a piece), so that one request's call fills the SMs too.
+// look at them.
 #include <stdint.h>
 #include <string.h>
 
 #include <algorithm>
+#include <exception>
+#include <functional>
 #include <limits>
-#include <new>
+#include <queue>
 #include <utility>
 #include <vector>
 
@@ -20,6 +21,99 @@
 namespace {
 
 using namespace segattn;
+
+// Costs in K tiles (1.34 us of a bf16 cache's bytes per SM).  A piece: start-up, first
+// scores, drain and epilogue, 7 us measured.  A merge: its launch, and per piece the
+// partial written and read back (128 rows x 512 bytes each way).
+constexpr int64_t kPieceCost = 5;
+constexpr double kMergeCost = 2.0, kMergePartCost = 0.023;
+
+// Where to cut the items along their keys: the cuts whose simulated schedule (pieces
+// longest first, each to the least loaded SM) plus merge is the shortest, among
+//   - every item in f equal pieces, f up to what gives each SM a few pieces;
+//   - whole waves of uncut items, and the items of the last, partly filled wave in f
+//     equal pieces;
+//   - the items end to end, cut wherever an SM's equal share of all K tiles ends.
+std::vector<std::vector<int32_t>> plan_cuts(const std::vector<PItem>& items) {
+  const size_t n = items.size();
+  using Cuts = std::vector<std::vector<int32_t>>;
+  auto equal = [&](size_t i, int64_t f, std::vector<int32_t>& ends) {
+    const int64_t t = items[i].tiles, p = std::max<int64_t>(1, std::min(f, t));
+    for (int64_t j = 1; j <= p; ++j) ends.push_back((int32_t)(t * j / p));
+  };
+  std::vector<Cuts> cands;
+  const int64_t most = std::min<int64_t>(
+      2 * kSmCount, std::max<int64_t>(4, 2 * kSmCount / std::max<int64_t>(1, (int64_t)n)));
+  for (int64_t f = 1; f <= most; ++f) {
+    Cuts c(n);
+    for (size_t i = 0; i < n; ++i) equal(i, f, c[i]);
+    cands.push_back(std::move(c));
+  }
+  std::vector<size_t> order(n);  // longest first
+  for (size_t i = 0; i < n; ++i) order[i] = i;
+  std::stable_sort(order.begin(), order.end(),
+                   [&](size_t a, size_t b) { return items[a].tiles > items[b].tiles; });
+  const size_t whole = n / kSmCount * kSmCount;
+  if (whole > 0 && whole < n)
+    for (int64_t f = 2; f <= 8; ++f) {
+      Cuts c(n);
+      for (size_t k = 0; k < n; ++k) equal(order[k], k < whole ? 1 : f, c[order[k]]);
+      cands.push_back(std::move(c));
+    }
+  int64_t total = 0;
+  for (const PItem& it : items) total += it.tiles;
+  if (total >= kSmCount) {
+    // a cut that would leave fewer than kShort tiles on one side is moved to the item's end
+    constexpr int64_t kShort = 4;
+    Cuts c(n);
+    int64_t at = 0;  // tiles before item k, longest first
+    for (size_t k = 0; k < n; ++k) {
+      const int64_t t = items[order[k]].tiles;
+      int64_t last = 0;
+      for (int64_t s = at * kSmCount / total + 1; s <= kSmCount; ++s) {
+        const int64_t cut = s * total / kSmCount - at;
+        if (cut >= t) break;
+        if (cut - last < kShort || t - cut < kShort) continue;
+        c[order[k]].push_back((int32_t)cut);
+        last = cut;
+      }
+      c[order[k]].push_back((int32_t)t);
+      at += t;
+    }
+    cands.push_back(std::move(c));
+  }
+  double best = std::numeric_limits<double>::max();
+  size_t pick = 0;
+  std::vector<int64_t> cost;
+  for (size_t k = 0; k < cands.size(); ++k) {
+    cost.clear();
+    int64_t parts = 0;
+    for (const std::vector<int32_t>& ends : cands[k]) {
+      int32_t from = 0;
+      for (int32_t e : ends) {
+        cost.push_back(e - from + kPieceCost);
+        from = e;
+      }
+      if (ends.size() > 1) parts += (int64_t)ends.size();
+    }
+    std::sort(cost.begin(), cost.end(), std::greater<int64_t>());
+    std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> sm;
+    for (int i = 0; i < kSmCount; ++i) sm.push(0);
+    int64_t span = 0;
+    for (int64_t c : cost) {
+      const int64_t t = sm.top() + c;
+      sm.pop();
+      sm.push(t);
+      span = std::max(span, t);
+    }
+    const double all = (double)span + (parts ? kMergeCost + kMergePartCost * (double)parts : 0.0);
+    if (all < best) {
+      best = all;
+      pick = k;
+    }
+  }
+  return std::move(cands[pick]);
+}
 
 int build(int batch, const int32_t* draft_lens, const int32_t* parents, const uint8_t* mask,
           const int32_t* seg_counts, const int32_t* seg_starts, const int32_t* seg_lens,
@@ -117,12 +211,9 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
     for (int32_t q0 = 0; q0 < t; q0 += span)
       for (int g = 0; g < kv_heads; ++g) items.push_back({r, g, q0, tiles, false, false});
   }
-  const int max_split =
-      items.empty() ? 1
-                    : (int)std::max<int64_t>(kMaxSplit, 2 * kSmCount / (int64_t)items.size());
   std::vector<Row4> no_citems;
   Pieces pieces;
-  plan_pieces(items, max_split, no_citems, pieces, kTreeMinPieceTiles);
+  emit_pieces(items, plan_cuts(items), no_citems, pieces);
   if (pieces.work.size() > (size_t)kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
 
   // ---- layout
