@@ -304,6 +304,13 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
   // second S buffer of tile 0, so the next tile's S = QK^T overlaps this tile's
   // softmax.
   constexpr bool single = SINGLE;
+  // Columns of O go through the epilogues 32 at a time.  Drafted tokens roll those loops: a
+  // CTA runs them once, so their instructions come from the second-level cache at best,
+  // and under a full memory load the unrolled form spent 4 to 10 us on fetching itself
+  // (64 trees of 16 over 4k keys, E4M3: 227 us unrolled, 196 rolled).  The long passes of
+  // the plain two-tile kernel keep them unrolled: rolled, its main loop came out of the
+  // compiler 6 % slower (2048 queries over 131072 keys, 7.38 -> 7.85 ms with the decode).
+  constexpr int kRoll = TREE || SINGLE ? 1 : D / 32;
   // TREE, item with queries in query tile 0 only (row word 6): both softmax groups work
   // on that tile, group t on K tiles t, t + 2, ... with an O of its own, and the two are
   // merged at the end.  (One group alone takes ~3200 cycles per K tile, exponentials,
@@ -442,6 +449,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
                            int cols, int panels, int bytes) {
         if (lane == 0) mbar_expect_tx(bar, tr.count * panels * bytes);
         __syncwarp();
+#pragma unroll
         for (int h = 0; h < panels; ++h) {
           uint8_t* at = dst + h * kHalfBytes + (tr.contiguous ? 0 : lane * 4 * bytes);
           if (tr.contiguous) {
@@ -898,7 +906,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
             !__all_sync(0xffffffffu, mbar_wait(o_full + t, (j - 1) & 1, abort_flag, wait_limit)))
           return false;
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll kRoll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * c, o);
@@ -1057,9 +1065,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     // shared memory (in the K ring, which is free then)
     float w_own = 1.f, w_other = 0.f;
     float2* other_ml = reinterpret_cast<float2*>(sK);
-    // 32 columns of this row's O (fp32).  The epilogues below walk them in rolled loops: a
-    // CTA runs them once, so their instructions come from the second-level cache at best,
-    // and under a full memory load the unrolled form spent 4 to 10 us on fetching itself.
+    // 32 columns of this row's O (fp32).
     auto load_o = [&](int c, uint32_t (&o)[32]) {
       if (n_tiles == 0) {
 #pragma unroll
@@ -1140,7 +1146,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
       const int64_t prow0 = (int64_t)slot * kItemRows + t * kTileRows + quad * 32;
       open_o();
-#pragma unroll 1
+#pragma unroll kRoll
       for (int pass = 0; pass < D / 32; ++pass) {
         uint32_t o[32];
         load_o(pass, o);
@@ -1167,7 +1173,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       constexpr int RPI = 32 / CH; // rows per warp instruction of the copy
       const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
       open_o();
-#pragma unroll 1
+#pragma unroll kRoll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         load_o(c, o);
@@ -1208,7 +1214,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       if (go) {
         const float inv = has_keys(l) ? (FP8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
         open_o();
-#pragma unroll 1
+#pragma unroll kRoll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           load_o(c, o);
