@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* nonfinite = reinterpret_cast<int*>(bars + 34);  // TREE: some drafted V value was not finite
+  volatile uint64_t* mask_at = bars + 36;  // TREE: first mask word of the request
   // limit of every bounded wait, read only when a wait checks it
   volatile uint64_t* wait_limit = reinterpret_cast<volatile uint64_t*>(bars + 29);
 
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     }
     *abort_flag = 0;
     *nonfinite = 0;
+    *mask_at = (uint64_t)(uint32_t)w3.y | ((uint64_t)(uint32_t)w3.z << 32);
     *wait_limit = p.wait_ns;
     fence_mbar_init();
   }
@@ -380,8 +382,30 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
             tma_load_3d(sK + h * kHalfBytes, &tm_k.box128, k_full, 64 * h, g, w3.x);
         }
       }
-      int seg = w2.w;
+      // The request's segments from the piece's first one on, 32 at a time, one per lane
+      // (loaded together: walking the arrays key by key is a chain of dependent loads,
+      // microseconds for a tile across a segment boundary).  Lane l: segment seg0 + l.
       const int seg_end = w1.w;
+      int seg0 = w2.w, seg_key, seg_off;  // first key; first slot minus first key
+      int seg_last;                       // key after the last one
+      auto load_segments = [&]() {
+        const int s = seg0 + lane;
+        const bool live = s < seg_end;
+        seg_key = live ? __ldg(p.tab.seg_kstart + s) : 0x7fffffff;
+        seg_off = live ? __ldg(p.tab.seg_start + s) - seg_key : 0;
+        seg_last = live ? seg_key + __ldg(p.tab.seg_len + s) : 0x7fffffff;
+      };
+      load_segments();
+      // lane of the segment that holds key j (the last one that starts at or before it)
+      auto segment_of = [&](int j) -> int {
+        for (;;) {
+          const uint32_t before = __ballot_sync(0xffffffffu, seg_key <= j);
+          const int l = 31 - __clz(before);
+          if (l < 31 || seg0 + 32 >= seg_end) return max(l, 0);
+          seg0 += 31;  // the window's last segment, and those after it
+          load_segments();
+        }
+      };
       // Pool rows of K tile i: lane l holds logical keys 4l .. 4l + 3 (keys past the
       // request are clamped to its last key).  Most tiles are 128 consecutive pool
       // slots (segments are long): one tiled box per 64-column half.  In a tile that
@@ -404,21 +428,41 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
         // consecutive pool slots -- one lookup, the same on every lane
         const int j0 = (kt0 + i) * kTileKeys;
         tr.count = kTileKeys;
-        while (seg + 1 < seg_end && __ldg(p.tab.seg_kstart + seg + 1) <= j0) ++seg;
-        const int ks = __ldg(p.tab.seg_kstart + seg);
-        if (j0 + kTileKeys <= ks + __ldg(p.tab.seg_len + seg)) {
-          tr.slot0 = __ldg(p.tab.seg_start + seg) + (j0 - ks);
+        int l = segment_of(j0);
+        int off = __shfl_sync(0xffffffffu, seg_off, l);
+        if (j0 + kTileKeys <= __shfl_sync(0xffffffffu, seg_last, l)) {
+          tr.slot0 = j0 + off;
           tr.contiguous = true;
           return;
         }
-        bool four = true;
+        const int last = min(j0 + kTileKeys, k_len) - 1;
+        int key[4], at[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = min(j0 + 4 * lane + e, k_len - 1);
-          while (seg + 1 < seg_end && __ldg(p.tab.seg_kstart + seg + 1) <= j) ++seg;
-          const int slot = __ldg(p.tab.seg_start + seg) + (j - __ldg(p.tab.seg_kstart + seg));
+          key[e] = min(j0 + 4 * lane + e, last);
+          at[e] = off;
+        }
+        // the segments that begin inside the tile
+        for (;;) {
+          if (++l == 32) {
+            if (seg0 + 32 >= seg_end) break;
+            seg0 += 31;  // keep the window's last segment: the next tile may begin in it
+            load_segments();
+            l = 1;
+          }
+          const int first = __shfl_sync(0xffffffffu, seg_key, l);
+          if (first > last) break;
+          off = __shfl_sync(0xffffffffu, seg_off, l);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key[e] >= first) at[e] = off;
+        }
+        bool four = true;
+        tr.slot0 = key[0] + at[0];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int slot = key[e] + at[e];
           tr.rows[e] = slot * p.kv_heads + g;
-          if (e == 0) tr.slot0 = slot;
           four &= slot == tr.slot0 + e;
         }
         // lanes whose rows are consecutive slots, and follow those of the lane before
@@ -750,13 +794,10 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     const int head = g * p.group + row % p.group;
     const bool row_valid = qi < q_len;
     const int prior = k_len - q_len;  // TREE: keys before the drafted ones
-    // TREE: this row's mask row.  Read anew where it is needed (the work row's words
-    // through a volatile access): kept in registers across the K tiles it would cost spills.
+    // TREE: this row's mask row.  Its address comes from shared memory where it is needed:
+    // in registers across the K tiles it would cost spills.
     auto mask_row = [&]() -> const uint32_t* {
-      const volatile uint32_t* w =
-          reinterpret_cast<const volatile uint32_t*>(p.tab.work + 4 * (p.work_base + blockIdx.x) + 3);
-      const uint64_t at = (uint64_t)w[1] | ((uint64_t)w[2] << 32);
-      return p.mask_base + at + (int64_t)qi * ((q_len + 31) >> 5);
+      return p.mask_base + *mask_at + (int64_t)qi * ((q_len + 31) >> 5);
     };
     if (TREE && row_valid) prefetch_global(mask_row());
     // TREE: which of the 32 keys from drafted key `at` on this row sees (at < 0: cached
@@ -816,6 +857,15 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
     // K tile i is this group's j-th (i = j unless dual).
     auto softmax_tile = [&](int i, int j, bool masked) -> bool {
       auto f = [](uint32_t bits) { return __uint_as_float(bits); };
+      // TREE: the tile's mask words, before the S row takes its 128 registers (bf16) or
+      // where they are used (FP8): the order that leaves the loop without spills
+      uint32_t words[4] = {0u, 0u, 0u, 0u};
+      auto load_words = [&]() {
+        const uint32_t* mrow = mask_row();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) words[c] = mask_word(mrow, (kt0 + i) * kTileKeys + 32 * c - prior);
+      };
+      if (TREE && !FP8 && masked) load_words();
       // the whole S row in registers: one round trip to tensor memory
       uint32_t sv[4][32];
       tmem_ld128(tS, sv);
@@ -829,10 +879,10 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
       }
       if (masked) {
         const int kb = (kt0 + i) * kTileKeys;
-        const uint32_t* mrow = TREE ? mask_row() : nullptr;
+        if (TREE && FP8) load_words();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint32_t word = TREE ? mask_word(mrow, kb + 32 * c - prior) : 0u;
+          const uint32_t word = TREE ? words[c] : 0u;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const bool hide = TREE ? !((word >> e) & 1u) : kb + 32 * c + e >= vis;

@@ -108,6 +108,51 @@ def test_long_context_in_many_pieces_and_segments():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("short", [1, 3, 40])
+def test_many_short_segments(fp8, short):
+    """More segments than a producer warp holds at once, inside one K tile and across tiles; empty
+    segments among them."""
+    rnd = random.Random(short)
+    draft, prior = [5, 17], [700, 1500]
+    c = ref.tree_case(rnd, draft, prior, 16, 2, 128, fp8=fp8)
+    starts, lens = [], []
+    for ss, ll in zip(c["seg_starts"], c["seg_lens"]):
+        s2, l2 = [], []
+        for s, l in zip(ss, ll):   # the same slots, cut into runs of up to `short` keys
+            at = 0
+            while at < l:
+                n = min(l - at, rnd.randint(1, short))
+                if rnd.random() < 0.2:
+                    s2.append(rnd.randrange(c["num_slots"]))
+                    l2.append(0)
+                s2.append(s + at)
+                l2.append(n)
+                at += n
+        starts.append(s2)
+        lens.append(l2)
+    # runs in another order: neighbouring keys no longer sit in neighbouring slots
+    for r in range(2):
+        order = list(range(len(starts[r])))
+        rnd.shuffle(order)
+        starts[r], lens[r] = [starts[r][i] for i in order], [lens[r][i] for i in order]
+    c["seg_starts"], c["seg_lens"] = starts, lens
+    assert len(starts[1]) > 32 or short == 40
+    check(c, f"runs of {short}", parents=[p for t in draft for p in ref.random_parents(rnd, t)])
+    # the plain prefill walks the same segments
+    hq, d = c["q"].shape[1:]
+    tab = sa.SegTable.build(draft, starts, lens, c["num_slots"], True, sa.MODE_PREFILL, hq, 2, d).to("cuda")
+    out, lse = torch.empty_like(c["q"]), torch.empty(22, hq, device="cuda")
+    ws = torch.empty(max(16, tab.workspace_bytes), dtype=torch.uint8, device="cuda")
+    if fp8:
+        sa.seg_attn_prefill_fp8(c["q"], c["k_pool"], c["v_pool"], c["k_scale"], c["v_scale"], out, lse,
+                                tab.device, tab.desc, c["scale"], ws)
+    else:
+        sa.seg_attn_prefill(c["q"], c["k_pool"], c["v_pool"], out, lse, tab.device, tab.desc, c["scale"], ws)
+    want = ref.tree(c["q"], c["k_values"], c["v_values"], draft, ref.visible(draft), starts, lens, c["scale"])
+    ref.check_tree(out, lse, want, "prefill")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_rows_that_see_nothing(fp8):
     """An empty mask row sees the cached keys only, or, without any, nothing: 0 and -inf."""
     draft, prior = [4, 3], [0, 200]
