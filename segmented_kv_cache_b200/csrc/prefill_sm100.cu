@@ -290,6 +290,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
   volatile uint64_t* wait_limit = reinterpret_cast<volatile uint64_t*>(bars + 29);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // drafted tokens: launched as a programmatic dependent, so that the launch itself
+  // overlaps the end of whatever ran before; nothing is read or written before this
+  if (TREE) grid_dependency_wait();
   // piece: keys tiles [kt0, kt1) of item (request, kv head g, query tiles from q0);
   // slot >= 0 when the item is split and this piece writes a partial result.  The
   // row also carries the request's first query row, queries, keys and the segment
@@ -1394,9 +1397,20 @@ int launch_items(const CUtensorMap& tq, const CUtensorMap& to, const PoolMaps& t
   if (cudaFuncSetAttribute(prefill_kernel<D, SINGLE, FP8, TMA_OUT, TREE>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SEG_ATTN_ERR_CUDA;
-  prefill_kernel<D, SINGLE, FP8, TMA_OUT, TREE>
-      <<<n, cta_threads<SINGLE, FP8>(), smem, stream>>>(tq, to, tk, tv, p);
-  return cudaGetLastError() == cudaSuccess ? SEG_ATTN_OK : SEG_ATTN_ERR_CUDA;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n);
+  cfg.blockDim = dim3(cta_threads<SINGLE, FP8>());
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = early;
+  cfg.numAttrs = TREE ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, prefill_kernel<D, SINGLE, FP8, TMA_OUT, TREE>, tq, to, tk, tv, p) ==
+                 cudaSuccess
+             ? SEG_ATTN_OK
+             : SEG_ATTN_ERR_CUDA;
 }
 
 template <int D, bool FP8, bool TREE>
