@@ -315,6 +315,9 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
   // the plain two-tile kernel keep them unrolled: rolled, its main loop came out of the
   // compiler 6 % slower (2048 queries over 131072 keys, 7.38 -> 7.85 ms with the decode).
   constexpr int kRoll = TREE || SINGLE ? 1 : D / 32;
+  // The rescale of O, rolled, does the same to every two-tile main loop (8 trees of 64 over
+  // 16k keys 244 -> 269 us); the one-tile kernel gains from it (a shared-prefix decode of 64 requests 0.268 -> 0.260 ms).
+  constexpr int kRollRescale = SINGLE ? 1 : D / 32;
   // TREE, item with queries in query tile 0 only (row word 6): both softmax groups work
   // on that tile, group t on K tiles t, t + 2, ... with an O of its own, and the two are
   // merged at the end.  (One group alone takes ~3200 cycles per K tile, exponentials,
@@ -959,7 +962,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
             !__all_sync(0xffffffffu, mbar_wait(o_full + t, (j - 1) & 1, abort_flag, wait_limit)))
           return false;
         tc_fence_after();
-#pragma unroll kRoll
+#pragma unroll kRollRescale
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * c, o);
