@@ -167,7 +167,8 @@ typedef struct seg_attn_tree_desc {
   int64_t off_mask;       /* mask rows, requests back to back: ceil(draft_len / 32) words
                              each, bit j of word w of row i: i sees drafted token 32 w + j */
   int64_t off_draft_slot; /* [total_q] pool slot of each drafted token */
-  seg_attn_table_desc pass; /* the prefill table of all keys (offsets into the same buffer);
+  seg_attn_table_desc pass; /* the prefill table of all keys (offsets into the same buffer;
+                               for the tree calls only: the plain ones refuse it);
                                words 13, 14 of a work row: first mask word of the request
                                (low and high half) */
   uint64_t table_bytes, workspace_bytes;

@@ -47,7 +47,8 @@ extern "C" int seg_attn_rope_plan(int rotary_dim, int layout, double base,
       if (!good(scaling->factors[i])) return SEG_ATTN_ERR_INVALID_ARG;
   }
   if (scaling && scaling->amp != 0.0) amp = scaling->amp;
-  if (!good(amp)) return SEG_ATTN_ERR_INVALID_ARG;
+  if (!good(amp) || !std::isfinite((float)amp) || !((float)amp > 0.f))
+    return SEG_ATTN_ERR_INVALID_ARG;
   long double ramp0 = 0.0L, ramp1 = 0.0L;  // YARN: pairs where the ramp starts and ends
   if (kind == SEG_ATTN_ROPE_SCALE_YARN) {
     auto pair = [&](long double turns) {

@@ -7,7 +7,6 @@
 #include <string.h>
 
 #include <algorithm>
-#include <exception>
 #include <functional>
 #include <limits>
 #include <queue>
@@ -231,7 +230,7 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   desc->off_mask = lay.take((int64_t)words.size());
   desc->off_draft_slot = lay.take(total_q);
 
-  p.magic = SEG_ATTN_TABLE_MAGIC;
+  p.magic = SEG_ATTN_TREE_MAGIC;  // not a table the plain calls take
   p.version = SEG_ATTN_TABLE_VERSION;
   p.mode = SEG_ATTN_MODE_PREFILL;
   p.batch = batch;
@@ -308,7 +307,7 @@ extern "C" int seg_attn_build_tree_table(int batch, const int32_t* draft_lens,
   try {
     rc = build(batch, draft_lens, parents, mask, seg_counts, seg_starts, seg_lens, num_slots,
                q_heads, kv_heads, head_dim, host_out, host_out_bytes, desc);
-  } catch (const std::exception&) {  // host memory: no exception leaves a C entry
+  } catch (...) {  // host memory: no exception leaves a C entry
     rc = SEG_ATTN_ERR_UNSUPPORTED;
   }
   // a failed build leaves nothing a compute call would accept; a too small buffer

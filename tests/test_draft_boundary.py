@@ -89,7 +89,9 @@ def test_plan_refusals():
                R("wavelength", factor=2.0, original_len=100, low=4.0, high=4.0),
                R("wavelength", factor=2.0, original_len=100, low=4.0, high=1.0),
                R("per_pair"), R("per_pair", factors=[1.0] * 31), R("per_pair", factors=[0.0] * 32),
-               R("linear", factor=2.0, amp=-1.0), R("bent")):
+               R("linear", factor=2.0, amp=-1.0), R("linear", factor=2.0, amp=1e300),
+               R("yarn", factor=1e-9, original_len=100),
+               R("bent")):
         assert code_of(lambda: plan(64, scaling=sc)) == S["INVALID_ARG"], sc
     assert sa.load_library().seg_attn_rope_plan(64, 2, 1e4, None, ctypes.byref(
         sa.seg_attn_rope_desc())) == S["INVALID_ARG"]
@@ -281,6 +283,8 @@ def test_compute_refusals_before_any_launch(lib):
     bad = sa.seg_attn_tree_desc.from_buffer_copy(tab.desc)
     bad.version = 99
     assert h(A, A, A, A, A, A, ctypes.byref(bad), 0.1, A, ws, None) == I
+    # the plain calls do not take the pass inside a tree table for one of theirs
+    assert lib.seg_attn_prefill(A, A, A, A, A, A, ctypes.byref(tab.desc.pass_), 0.1, A, ws, None) == I
     empty = build([0], [[(0, 5)]])
     assert h(None, None, None, None, None, None, ctypes.byref(empty.desc), 0.1, None, 0, None) == 0
 

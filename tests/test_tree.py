@@ -108,6 +108,24 @@ def test_long_context_in_many_pieces_and_segments():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("draft", [4, 40])
+def test_a_copy_that_never_lands_is_an_error_not_a_hang(fp8, draft):
+    """The stall test withholds K tile 2: every CTA gives up after 1 ms (one query tile, whose two
+    softmax groups meet at the end, and two), the error word says so, and the next call is right."""
+    c = ref.tree_case(random.Random(15), [draft] * 20, [1500] * 20, 64, 8, 128, fp8=fp8)
+    tab = table(c)
+    assert tab.desc.pass_.max_k_tiles > 2
+    sa.seg_attn_stall_test(2, 1000)
+    try:
+        run(c, tab)
+        torch.cuda.synchronize()
+        assert sa.seg_attn_take_device_error() == 1
+    finally:
+        sa.seg_attn_stall_test(-1, 1000000)
+    check(c)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("short", [1, 3, 40])
 def test_many_short_segments(fp8, short):
     """More segments than a producer warp holds at once, inside one K tile and across tiles; empty
