@@ -21,11 +21,13 @@ namespace {
 
 using namespace segattn;
 
-// Costs in K tiles (1.34 us of a bf16 cache's bytes per SM).  A piece: start-up, first
-// scores, drain and epilogue, 7 us measured.  A merge: its launch, and per piece the
-// partial written and read back (128 rows x 512 bytes each way).
-constexpr int64_t kPieceCost = 5;
-constexpr double kMergeCost = 2.0, kMergePartCost = 0.023;
+// Costs in tenths of the time a K tile of an item with one query tile takes (1.34 us: a
+// bf16 cache's bytes at one SM's share of memory).  A K tile of an item with two query
+// tiles takes 1.9 us (its softmax).  A piece: start-up, first scores, drain and epilogue,
+// 7 us measured.  A merge: its launch, and per piece the partial written and read back
+// (128 rows x 512 bytes each way per query tile).
+constexpr int64_t kTileCost = 10, kTwoTileCost = 14, kPieceCost = 50;
+constexpr double kMergeCost = 20.0, kMergePartCost = 0.23;
 // The uncut plan is taken when it is this near the best: while memory bounds the pass,
 // idle SMs cost less than the simulation says (32 trees of 16 over 8k keys: uncut 186 us,
 // the plan simulated 4 % shorter 201).
@@ -37,13 +39,16 @@ constexpr double kUncutSlack = 1.08;
 //   - whole waves of uncut items, and the items of the last, partly filled wave in f
 //     equal pieces;
 //   - the items end to end, cut wherever an SM's equal share of all K tiles ends.
-std::vector<std::vector<int32_t>> plan_cuts(const std::vector<PItem>& items) {
+// `one_tile[i]`: item i has queries in its first query tile only.
+std::vector<std::vector<int32_t>> plan_cuts(const std::vector<PItem>& items,
+                                            const std::vector<char>& one_tile) {
   const size_t n = items.size();
   using Cuts = std::vector<std::vector<int32_t>>;
   auto equal = [&](size_t i, int64_t f, std::vector<int32_t>& ends) {
     const int64_t t = items[i].tiles, p = std::max<int64_t>(1, std::min(f, t));
     for (int64_t j = 1; j <= p; ++j) ends.push_back((int32_t)(t * j / p));
   };
+  auto tile_cost = [&](size_t i) { return one_tile[i] ? kTileCost : kTwoTileCost; };
   std::vector<Cuts> cands;
   const int64_t most = std::min<int64_t>(
       2 * kSmCount, std::max<int64_t>(4, 2 * kSmCount / std::max<int64_t>(1, (int64_t)n)));
@@ -55,7 +60,9 @@ std::vector<std::vector<int32_t>> plan_cuts(const std::vector<PItem>& items) {
   std::vector<size_t> order(n);  // longest first
   for (size_t i = 0; i < n; ++i) order[i] = i;
   std::stable_sort(order.begin(), order.end(),
-                   [&](size_t a, size_t b) { return items[a].tiles > items[b].tiles; });
+                   [&](size_t a, size_t b) {
+                     return items[a].tiles * tile_cost(a) > items[b].tiles * tile_cost(b);
+                   });
   const size_t whole = n / kSmCount * kSmCount;
   if (whole > 0 && whole < n)
     for (int64_t f = 2; f <= 8; ++f) {
@@ -64,24 +71,24 @@ std::vector<std::vector<int32_t>> plan_cuts(const std::vector<PItem>& items) {
       cands.push_back(std::move(c));
     }
   int64_t total = 0;
-  for (const PItem& it : items) total += it.tiles;
-  if (total >= kSmCount) {
+  for (size_t i = 0; i < n; ++i) total += items[i].tiles * tile_cost(i);
+  if (total >= kSmCount * kTwoTileCost) {
     // a cut that would leave fewer than kShort tiles on one side is moved to the item's end
     constexpr int64_t kShort = 4;
     Cuts c(n);
-    int64_t at = 0;  // tiles before item k, longest first
+    int64_t at = 0;  // cost before item k, longest first
     for (size_t k = 0; k < n; ++k) {
-      const int64_t t = items[order[k]].tiles;
+      const int64_t t = items[order[k]].tiles, w = tile_cost(order[k]);
       int64_t last = 0;
       for (int64_t s = at * kSmCount / total + 1; s <= kSmCount; ++s) {
-        const int64_t cut = s * total / kSmCount - at;
+        const int64_t cut = (s * total / kSmCount - at) / w;
         if (cut >= t) break;
         if (cut - last < kShort || t - cut < kShort) continue;
         c[order[k]].push_back((int32_t)cut);
         last = cut;
       }
       c[order[k]].push_back((int32_t)t);
-      at += t;
+      at += t * w;
     }
     cands.push_back(std::move(c));
   }
@@ -89,13 +96,14 @@ std::vector<std::vector<int32_t>> plan_cuts(const std::vector<PItem>& items) {
   std::vector<int64_t> cost, parts(cands.size(), 0);
   for (size_t k = 0; k < cands.size(); ++k) {
     cost.clear();
-    for (const std::vector<int32_t>& ends : cands[k]) {
+    for (size_t i = 0; i < n; ++i) {
+      const std::vector<int32_t>& ends = cands[k][i];
       int32_t from = 0;
       for (int32_t e : ends) {
-        cost.push_back(e - from + kPieceCost);
+        cost.push_back((e - from) * tile_cost(i) + kPieceCost);
         from = e;
       }
-      if (ends.size() > 1) parts[k] += (int64_t)ends.size();
+      if (ends.size() > 1) parts[k] += (int64_t)ends.size() * (one_tile[i] ? 1 : 2);
     }
     std::sort(cost.begin(), cost.end(), std::greater<int64_t>());
     std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> sm;
@@ -203,17 +211,21 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   const int32_t qpt = kTileRows / group;
   const int32_t span = qpt * kTilesPerItem;
   std::vector<PItem> items;
+  std::vector<char> one_tile;  // both softmax groups take the item's one query tile
   int32_t max_k_tiles = 0;
   for (int r = 0; r < batch; ++r) {
     const int32_t t = q_off[r + 1] - q_off[r];
     const int32_t tiles = (int32_t)(((int64_t)keys[r] + kTileKeys - 1) / kTileKeys);
     max_k_tiles = std::max(max_k_tiles, tiles);
     for (int32_t q0 = 0; q0 < t; q0 += span)
-      for (int g = 0; g < kv_heads; ++g) items.push_back({r, g, q0, tiles, false, false});
+      for (int g = 0; g < kv_heads; ++g) {
+        items.push_back({r, g, q0, tiles, false, false});
+        one_tile.push_back(t - q0 <= qpt);
+      }
   }
   std::vector<Row4> no_citems;
   Pieces pieces;
-  emit_pieces(items, plan_cuts(items), no_citems, pieces);
+  emit_pieces(items, plan_cuts(items, one_tile), no_citems, pieces);
   if (pieces.work.size() > (size_t)kI32Max) return SEG_ATTN_ERR_UNSUPPORTED;
 
   // ---- layout
