@@ -15,9 +15,9 @@
 // TMA gather4 (four pool rows per instruction) where they do not.  Keys past
 // the end of the request are clamped to its last key and masked.
 //
-// Warp roles (two query tiles: 10 warps, 12 over an FP8 cache; one: 6 and 10):
+// Warp roles (two query tiles: 10 warps, 12 over an FP8 cache; one: 6 and 8):
 //   warp 0       TMA producer: Q tiles once, then a K ring and a V ring
-//                (stages per variant below), K tile i + 1 before V tile i.
+//                (depths below), K tile i + 1 before V tile i.
 //   warp 1       TMEM allocator and MMA issuer: the whole warp runs the issue
 //                loop, one elected lane executes each tcgen05.mma / commit.
 //   warps 2-5    softmax for query tile 0, warps 6-9 for tile 1: one thread
@@ -41,10 +41,11 @@
 // One query tile: S double-buffered, each buffer with a P region of its own, so
 // the QK that refills an S buffer never overwrites what the PV before it reads.
 // TMEM columns: O [0,128) P0 [128,192) P1 [192,256) S0 [256,384) S1 [384,512).
-// Over an FP8 cache the last two warps widen the E4M3 codes to f16 in place, inside
-// the ring slot whose second half the codes were loaded into.
-// (A single staging tile per K and V, as the one-tile kernel had, exposed every tile's
-// load latency: 64 trees of 16 over 4k keys, 308 us against 87 us of cache reads.)
+// Over an FP8 cache the last two warps widen the E4M3 codes of K and of V tiles to f16
+// in place, inside the ring slot whose second half the codes were loaded into.  (A single staging tile per K and V, as the one-tile kernel had, exposed every tile's
+// load latency: 64 trees of 16 over 4k keys, 308 us; now 200.)
+// Drafted tokens (TREE, see the kernel's comment): masks of bits on the last K tiles, and
+// items of one query tile run both softmax groups on it.
 // Every mbarrier wait is bounded (1 s); a timeout stops all roles of the CTA,
 // drains in-flight copies and MMAs, frees TMEM and flags a device error.
 #include <cuda.h>

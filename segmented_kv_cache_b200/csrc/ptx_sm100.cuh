@@ -374,13 +374,6 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, bool b_mn_maj
   return idesc_bf16_f32(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
-// Two E4M3 codes (low byte first) -> two f16 (exact: every E4M3 value is an f16).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
-  uint32_t y;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<unsigned short>(two_codes)));
-  return y;
-}
-
 // Four E4M3 codes -> four f16 (exact), both halves converted from one register.
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\t"
