@@ -477,3 +477,56 @@ def test_masked_nan_codes_in_an_e4m3_cache():
                 hit[sees, 16:24] = True
                 assert torch.equal(torch.isnan(lse), hit[..., 0])
             assert bool(same[~hit].all()) and bool(torch.isnan(out[hit]).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_slots_past_two_to_the_31_values(fp8):
+    """Rows at the end of a pool of more than 2^31 values: every call writes and reads what it
+    does in a small pool, bit for bit, a drafted NaN (its rows are read by address) included."""
+    rnd = random.Random(21)
+    hq, hk, d, far = 64, 8, 128, 2_200_000
+    draft, prior = [40, 9], [500, 1500]
+    c = ref.tree_case(rnd, draft, prior, hq, hk, d, fp8=fp8)
+    n, S = sum(draft), c["num_slots"]
+    parents = [p for t in draft for p in ref.random_parents(rnd, t)]
+    drafted = []
+    for r, t in enumerate(draft):
+        keys = [s + i for s, l in zip(c["seg_starts"][r], c["seg_lens"][r]) for i in range(l)]
+        drafted += keys[len(keys) - t:]
+    base = far - S
+    g = torch.Generator().manual_seed(22)
+    new = torch.randn(n, hk, d, generator=g).to(torch.bfloat16).cuda()
+    values = new.clone()
+    values[7, 3, 50] = math.nan
+    pos = torch.randint(0, 1 << 20, (n,), generator=g, dtype=torch.int32).cuda()
+    plan = sa.seg_attn_rope_plan(d)
+
+    def steps(case, shift):
+        at = torch.tensor(drafted, dtype=torch.int32, device="cuda") + shift
+        q = torch.empty_like(case["q"])
+        if fp8:
+            sa.seg_attn_rope_append_fp8(case["q"], q, new, values, pos, at, plan, case["k_scale"],
+                                        case["v_scale"], case["k_pool"], case["v_pool"])
+        else:
+            sa.seg_attn_rope_append(case["q"], q, new, values, pos, at, plan, case["k_pool"],
+                                    case["v_pool"])
+        tab = sa.TreeTable.build(draft, [[s + shift for s in x] for x in case["seg_starts"]],
+                                 case["seg_lens"], case["num_slots"], hq, hk, d,
+                                 parents=parents).to("cuda")
+        out, lse = run(dict(case, q=q), tab)
+        sa.seg_attn_kv_move(case["k_pool"], case["v_pool"], at[:5].clone(), at[20:25].clone())
+        return out, lse
+
+    big = dict(c, num_slots=far)
+    for name in ("k_pool", "v_pool"):
+        big[name] = torch.empty(far, hk, d, dtype=c[name].dtype, device="cuda")
+        big[name][base:] = c[name]
+    assert big["k_pool"].numel() > 1 << 31
+    o0, l0 = steps(c, 0)
+    o1, l1 = steps(big, base)
+    assert torch.equal(torch.isnan(o0), torch.isnan(o1)) and bool(torch.isnan(o0).any())
+    assert torch.equal(o0.view(torch.int16), o1.view(torch.int16)) and torch.equal(l0, l1)
+    kind = torch.uint8 if fp8 else torch.int16
+    for name in ("k_pool", "v_pool"):
+        assert torch.equal(big[name][base:].view(kind), c[name].view(kind))
+    assert sa.seg_attn_take_device_error() == 0
