@@ -131,7 +131,8 @@ int seg_attn_rope_append(const void* q, int64_t q_stride, void* q_out, int64_t q
  * seg_attn_rope_append_fp8 -- the same into E4M3 pools: code =
  * round-to-nearest-even(value / scale[head]) saturated to +-448, with the
  * rotated key rounded once, from fp32 (seg_attn_kv_append_fp8's codes for an
- * unrotated value).
+ * unrotated value).  Scales are device values, finite and > 0 (a head of zeros
+ * takes any positive one); they are not checked.
  */
 int seg_attn_rope_append_fp8(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
                              const void* k_new, int64_t k_stride, const void* v_new,
@@ -192,7 +193,7 @@ size_t seg_attn_tree_workspace_size(const seg_attn_tree_desc* desc);
 /*
  * seg_attn_tree / seg_attn_tree_fp8 -- arguments as seg_attn_prefill /
  * seg_attn_prefill_fp8, with a tree table.  Two calls that may overlap on the
- * GPU need workspaces of their own.
+ * GPU need workspaces of their own.  Scales as in seg_attn_rope_append_fp8.
  */
 int seg_attn_tree(const void* q, const void* k_pool, const void* v_pool, void* out, float* lse,
                   const void* dev_table, const seg_attn_tree_desc* desc, float softmax_scale,
