@@ -111,10 +111,12 @@ __device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
 
 // x / scale, rounded as the division is: a product with the rounded reciprocal, then one
 // correction by the remainder (Markstein's theorem: correctly rounded when the
-// reciprocal is).  An infinite or NaN product has no remainder and is kept.
+// reciprocal is).  The remainder is taken with the product's sign (q scale - x), so that a
+// zero one adds -0 and a product of -0 stays -0, whose code is 0x80.  An infinite or NaN
+// product has no remainder and is kept.
 __device__ __forceinline__ float quotient(float x, float scale, float reciprocal) {
   const float q = x * reciprocal;
-  const float r = fmaf(fmaf(-q, scale, x), reciprocal, q);
+  const float r = fmaf(fmaf(q, scale, -x), -reciprocal, q);
   return fabsf(q) < 3.0e38f ? r : q;
 }
 // E4M3 codes of four values over the head's scale, as seg_attn_kv_append_fp8's.

@@ -304,3 +304,42 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(sa.SegAttnError) as e:
             f()
         assert e.value.code == sa.STATUS["INVALID_ARG"], i
+
+
+@pytest.mark.parametrize("r", [64, 20])   # the vector kernel and the element-wise one
+@pytest.mark.parametrize("inter", [False, True])
+def test_unrotated_codes_are_the_plain_appends(r, inter):
+    """Zeros of both signs, infinities, NaN, saturating and tiny values, and scales on both sides
+    of the range where the quotient is a corrected product: V rows and the unrotated tail of K
+    rows take seg_attn_kv_append_fp8's codes, which are within half a step of the division."""
+    g = torch.Generator().manual_seed(10)
+    scales = [1 / 16, 0.0371, 1e-17, 1.7e-19, 3e-24, 6e16, 2.3e19, 1e-39]
+    n, hk, d = 64, len(scales), 128
+    S = n + 5
+    s = torch.tensor(scales, dtype=torch.float32)
+    kv = (torch.randn(n, 2 * hk, d, generator=g) * s.repeat(2)[:, None] * 60).to(torch.bfloat16)
+    tail = torch.tensor([-0.0, 0.0, math.inf, -math.inf, math.nan, 3e38, -3e38, 1e-40, -1e-40,
+                         1e-38, -1e-38, 448.0, -448.0])
+    for h in range(2 * hk):
+        kv[h % n, h, -len(tail):] = tail.to(torch.bfloat16)
+        kv[(h + 20) % n, h, -8:] = torch.tensor([-0.0, 0.0] * 4).to(torch.bfloat16)
+    k, v = kv[:, :hk].contiguous().cuda(), kv[:, hk:].contiguous().cuda()
+    slots = torch.randperm(S, generator=g)[:n].to(torch.int32).cuda()
+    pos, sd = positions(g, n).cuda(), s.cuda()
+    a = [torch.full((S, hk, d), 0x55, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    sa.seg_attn_rope_append_fp8(None, None, k, v, pos, slots, sa.seg_attn_rope_plan(r, interleaved=inter),
+                                sd, sd, a[0], a[1])
+    sa.seg_attn_kv_append_fp8(k, v, slots, sd, sd, a[2], a[3])
+    assert torch.equal(a[1], a[3])
+    assert torch.equal(a[0][..., r:], a[2][..., r:])
+    got = a[1][slots.long()].cpu()
+    x = kv[:, hk:].double() / s.double()[:, None]
+    zero = x == 0
+    assert bool(zero.any()) and torch.equal(got[zero], torch.where(torch.signbit(x[zero]), 0x80, 0).to(torch.uint8))
+    nan = torch.isnan(x)
+    assert bool(((got[nan] & 0x7F) == 0x7F).all())
+    value = got.view(torch.float8_e4m3fn).double()
+    # half a step of a normal code or of a subnormal one
+    off = (value - x.clamp(-448, 448)).abs()[~nan]
+    assert bool((off <= ref.E4M3_HALF * x[~nan].abs().clamp(max=448) + 2.0 ** -10).all())
+    assert sa.seg_attn_take_device_error() == 0
