@@ -316,9 +316,6 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
   // the plain two-tile kernel keep them unrolled: rolled, its main loop came out of the
   // compiler 6 % slower (2048 queries over 131072 keys, 7.38 -> 7.85 ms with the decode).
   constexpr int kRoll = TREE || SINGLE ? 1 : D / 32;
-  // The rescale of O, rolled, does the same to every two-tile main loop (8 trees of 64 over
-  // 16k keys 244 -> 269 us); the one-tile kernel gains from it (a shared-prefix decode of 64 requests 0.268 -> 0.260 ms).
-  constexpr int kRollRescale = SINGLE ? 1 : D / 32;
   // TREE, item with queries in query tile 0 only (row word 6): both softmax groups work
   // on that tile, group t on K tiles t, t + 2, ... with an O of its own, and the two are
   // merged at the end.  (One group alone takes ~3200 cycles per K tile, exponentials,
@@ -389,12 +386,21 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
             tma_load_3d(sK + h * kHalfBytes, &tm_k.box128, k_full, 64 * h, g, w3.x);
         }
       }
-      // The request's segments from the piece's first one on, 32 at a time, one per lane
-      // (loaded together: walking the arrays key by key is a chain of dependent loads,
-      // microseconds for a tile across a segment boundary).  Lane l: segment seg0 + l.
+      // The segment that the last tile inside one segment lay in: key after it, first slot
+      // minus first key.  Long segments need no other lookup: two compares a tile (a search
+      // in the window below for every tile slowed one-tile items by 2 %).
       const int seg_end = w1.w;
-      int seg0 = w2.w, seg_key, seg_off;  // first key; first slot minus first key
-      int seg_last;                       // key after the last one
+      int seg0 = w2.w;
+      const int key0 = __ldg(p.tab.seg_kstart + seg0);
+      int cur_last = key0 + __ldg(p.tab.seg_len + seg0);
+      int cur_off = __ldg(p.tab.seg_start + seg0) - key0;
+      // The request's segments from there on, 32 at a time, one per lane, once a tile
+      // leaves that segment (loaded together: walking the arrays key by key is a chain of
+      // dependent loads, microseconds for a tile across a segment boundary).  Lane l:
+      // segment seg0 + l.
+      bool window = false;
+      int seg_key, seg_off;  // first key; first slot minus first key
+      int seg_last;          // key after the last one
       auto load_segments = [&]() {
         const int s = seg0 + lane;
         const bool live = s < seg_end;
@@ -402,7 +408,6 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
         seg_off = live ? __ldg(p.tab.seg_start + s) - seg_key : 0;
         seg_last = live ? seg_key + __ldg(p.tab.seg_len + s) : 0x7fffffff;
       };
-      load_segments();
       // lane of the segment that holds key j (the last one that starts at or before it)
       auto segment_of = [&](int j) -> int {
         for (;;) {
@@ -431,13 +436,23 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
         bool contiguous;
       };
       auto tile_rows = [&](int i, TileRows& tr) {
-        // the usual case: all 128 keys inside the segment of the first one, i.e. 128
-        // consecutive pool slots -- one lookup, the same on every lane
+        // the usual case: all 128 keys inside one segment, i.e. 128 consecutive pool
+        // slots, the same on every lane
         const int j0 = (kt0 + i) * kTileKeys;
         tr.count = kTileKeys;
+        if (j0 + kTileKeys <= cur_last) {
+          tr.slot0 = j0 + cur_off;
+          tr.contiguous = true;
+          return;
+        }
+        if (!window) load_segments();
+        window = true;
         int l = segment_of(j0);
         int off = __shfl_sync(0xffffffffu, seg_off, l);
-        if (j0 + kTileKeys <= __shfl_sync(0xffffffffu, seg_last, l)) {
+        const int end = __shfl_sync(0xffffffffu, seg_last, l);
+        if (j0 + kTileKeys <= end) {
+          cur_last = end;
+          cur_off = off;
           tr.slot0 = j0 + off;
           tr.contiguous = true;
           return;
@@ -495,17 +510,26 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
           tr.count = min(kTileKeys, (left + 3) & ~3);
         }
       };
-      // the rows of a tile, `bytes` each, `cols` columns per box and `panels` of them
+      // the rows of a tile, `bytes` each, `cols` columns per box and `panels` of them.  A
+      // contiguous tile has a path of its own: tested inside the panel loop, with the
+      // warp's step before it, long one-tile items took 3 % more.
       auto load_rows = [&](const TileRows& tr, uint8_t* dst, const PoolMaps& map, uint64_t* bar,
                            int cols, int panels, int bytes) {
+        if (tr.contiguous) {
+          if (lane == 0) {
+            mbar_expect_tx(bar, kTileKeys * panels * bytes);
+#pragma unroll
+            for (int h = 0; h < panels; ++h)
+              tma_load_3d(dst + h * kHalfBytes, &map.box128, bar, cols * h, g, tr.slot0);
+          }
+          return;
+        }
         if (lane == 0) mbar_expect_tx(bar, tr.count * panels * bytes);
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < panels; ++h) {
-          uint8_t* at = dst + h * kHalfBytes + (tr.contiguous ? 0 : lane * 4 * bytes);
-          if (tr.contiguous) {
-            if (lane == 0) tma_load_3d(at, &map.box128, bar, cols * h, g, tr.slot0);
-          } else if (tr.kind == kBox32) {
+          uint8_t* at = dst + h * kHalfBytes + lane * 4 * bytes;
+          if (tr.kind == kBox32) {
             tma_load_3d(at, &map.box32, bar, cols * h, g, tr.slot0);
           } else if (tr.kind == kBox8) {
             tma_load_3d(at, &map.box8, bar, cols * h, g, tr.slot0);
@@ -963,7 +987,7 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
             !__all_sync(0xffffffffu, mbar_wait(o_full + t, (j - 1) & 1, abort_flag, wait_limit)))
           return false;
         tc_fence_after();
-#pragma unroll kRollRescale
+#pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * c, o);
