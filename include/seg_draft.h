@@ -98,7 +98,8 @@ int seg_attn_rope_plan(int rotary_dim, int layout, double base,
  *   x, out       bf16, `heads` heads of head_dim consecutive values per token;
  *                token t starts at t * x_stride (out_stride) elements, so x may
  *                be the query part of a fused projection.  out may be x with the
- *                same stride (in place); otherwise they must not overlap.
+ *                same stride (in place; another stride is refused); otherwise
+ *                they must not overlap.
  *   positions    int32 [n_tokens] (device); any value, negative ones included
  *   backward     0: the rotation above; 1: its transpose (the gradient of x
  *                given the gradient of out)

@@ -402,6 +402,9 @@ int run(RopeParams& p, const seg_attn_rope_desc* rope, bool fp8, bool backward, 
   if (p.n_tokens > 1 && ((p.q_heads > 0 && (p.q_stride < qw || p.q_out_stride < qw)) ||
                          (p.kv_heads > 0 && (p.k_stride < kw || p.v_stride < kw))))
     return SEG_ATTN_ERR_INVALID_ARG;
+  // in place with another stride, a token's output would lie over other tokens' input
+  if (p.n_tokens > 1 && p.q_heads > 0 && p.q && p.q == p.q_out && p.q_stride != p.q_out_stride)
+    return SEG_ATTN_ERR_INVALID_ARG;
   if (p.n_tokens == 0 || p.q_heads + p.kv_heads == 0) return SEG_ATTN_OK;
   if (p.n_tokens > INT32_MAX) return SEG_ATTN_ERR_UNSUPPORTED;
   auto some = [](const void* x, uintptr_t a) { return x && aligned(x, a); };

@@ -302,3 +302,18 @@ def test_binding_checks_dtypes_shapes_and_devices():
     tab = build([2], [[(0, 5)]], num_slots=8, hq=4, hkv=4)
     assert code_of(lambda: sa.seg_attn_tree(x, pool, pool, x, None, tab.host, tab.desc, 0.1)) == \
         S["INVALID_ARG"]
+
+
+def test_in_place_needs_one_stride(lib):
+    """x and out at one address with different token strides would read rows already written."""
+    A, B = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 24)
+    R = ctypes.byref(sa.seg_attn_rope_plan(64))
+    I = S["INVALID_ARG"]
+    for x, y in ((512, 768), (768, 512)):
+        assert lib.seg_attn_rope(A, x, A, y, B, 2, 4, 128, R, 0, None) == I
+        assert lib.seg_attn_rope_append(A, x, A, y, B, 256, B, 256, B, B, 2, 4, 2, 128, R, B, B, 10,
+                                        None) == I
+        assert lib.seg_attn_rope_append_fp8(A, x, A, y, B, 256, B, 256, B, B, 2, 4, 2, 128, R, B, B, B,
+                                            B, 10, None) == I
+    # no rows: nothing to refuse
+    assert lib.seg_attn_rope(A, 512, A, 768, B, 0, 4, 128, R, 0, None) == 0
