@@ -754,18 +754,20 @@ class TreeTable:
         return seg_attn_tree_workspace_size(self.desc)
 
 
+# q_heads, kv_heads, head_dim, num_slots, total_q of the pass of a tree table
+_tree_sizes = struct.Struct("=3i2q").unpack_from
+_tree_sizes_at = seg_attn_tree_desc.pass_.offset + seg_attn_table_desc.q_heads.offset
+
+
 def _tree(fn, q, k_pool, v_pool, scales, out, lse, dev_table, desc, softmax_scale, workspace,
           stream):
     dev = _cuda_device(fn, "q", q, 3)
-    sizes = getattr(desc, "_sizes", None)
-    if sizes is None:   # values of q, of lse, of a pool, kv heads, table bytes (read once)
-        p = desc.pass_
-        sizes = desc._sizes = (p.total_q * p.q_heads * p.head_dim, p.total_q * p.q_heads,
-                               p.num_slots * p.kv_heads * p.head_dim, p.kv_heads, desc.table_bytes)
-    nq, nl, pool, hk, table_bytes = sizes
+    # read from the descriptor at every call: the caller may have refilled it
+    hq, hk, d, slots, total_q = _tree_sizes(desc, _tree_sizes_at)
+    nq, nl, pool = total_q * hq * d, total_q * hq, slots * hk * d
     kind = _BF16 if scales is None else _U8
     table = _ptr(fn, "dev_table", dev_table, _I32, dev)
-    if dev_table.numel() * 4 < table_bytes:
+    if dev_table.numel() * 4 < desc.table_bytes:
         _bad(fn, "dev_table is shorter than the table")
     scale_ptrs = () if scales is None else tuple(
         _ptr(fn, "scales", t, _F32, dev, hk) for t in scales)

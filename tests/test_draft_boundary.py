@@ -317,3 +317,38 @@ def test_in_place_needs_one_stride(lib):
                                             B, 10, None) == I
     # no rows: nothing to refuse
     assert lib.seg_attn_rope(A, 512, A, 768, B, 0, 4, 128, R, 0, None) == 0
+
+
+def test_sizes_follow_a_refilled_descriptor(lib, monkeypatch):
+    """The binding checks tensors against the descriptor as it is now: refilled through the C
+    entry for a larger table, the smaller table's tensors are refused and the larger one's pass
+    (the call itself is replaced: nothing is launched)."""
+    P = ctypes.c_void_p
+    i32 = lambda x: np.array(x, dtype=np.int32)
+    desc, called = sa.seg_attn_tree_desc(), []
+    monkeypatch.setattr(sa, "_cuda_device", lambda fn, name, t, dim: -1)
+    monkeypatch.setattr(sa, "_invoke", lambda fn, dev, stream, args: called.append(fn))
+
+    def fill(draft, keys, slots, hq, hk, d):
+        dl, sc, ss, sl = i32([draft]), i32([1]), i32([0]), i32([keys])
+        args = [1, P(dl.ctypes.data), None, None, P(sc.ctypes.data), P(ss.ctypes.data),
+                P(sl.ctypes.data), slots, hq, hk, d]
+        assert lib.seg_attn_build_tree_table(*args, None, 0, ctypes.byref(desc)) == 0
+        bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+        return dict(q=bf(draft, hq, d), k_pool=bf(slots, hk, d), v_pool=bf(slots, hk, d),
+                    out=bf(draft, hq, d), lse=torch.zeros(draft, hq), desc=desc, softmax_scale=0.1,
+                    dev_table=torch.zeros(desc.table_bytes // 4, dtype=torch.int32))
+
+    small = fill(3, 40, 50, 4, 2, 64)
+    sa.seg_attn_tree(**small)
+    large = fill(9, 400, 500, 8, 4, 128)
+    sa.seg_attn_tree(**large)
+    assert len(called) == 2
+    for name in ("q", "k_pool", "v_pool", "out", "lse", "dev_table"):
+        assert code_of(lambda: sa.seg_attn_tree(**{**large, name: small[name]})) == S["INVALID_ARG"], name
+    scales = lambda n: dict(k_scale=torch.ones(n), v_scale=torch.ones(n))
+    codes = {k: large[k].view(torch.uint8)[..., :128] for k in ("k_pool", "v_pool")}
+    codes = {k: v.contiguous() for k, v in codes.items()}
+    sa.seg_attn_tree_fp8(**{**large, **codes, **scales(4)})
+    assert code_of(lambda: sa.seg_attn_tree_fp8(**{**large, **codes, **scales(2)})) == S["INVALID_ARG"]
+    assert len(called) == 3
