@@ -156,3 +156,71 @@ def tree_case(rnd, draft, prior, hq, hkv, d, nseg=3, fp8=False, device="cuda", e
             c[name + "_pool"] = x.to(torch.bfloat16).to(device)
             c[name + "_values"] = c[name + "_pool"]
     return c
+
+
+def request_slots(c, r, device=None):
+    """Pool slots of request r's keys, in logical order."""
+    runs = [torch.arange(s, s + l) for s, l in zip(c["seg_starts"][r], c["seg_lens"][r])]
+    return torch.cat(runs).to(device if device is not None else c["q"].device)
+
+
+def plant(c, targets, factor):
+    """Make row (token i, head h) of a one-request case look at one key: the key of logical
+    position targets[i * group + h % group] becomes `factor` times the row's query, which
+    outweighs all random keys together.  Changes k_pool and k_values in place."""
+    t, hq, _ = c["q"].shape
+    hkv = c["k_pool"].shape[1]
+    group = hq // hkv
+    slots = request_slots(c, 0)[torch.tensor(targets, device=c["q"].device)]
+    for g in range(hkv):
+        rows = c["q"][:, g * group:(g + 1) * group].reshape(t * group, -1)[:len(targets)].float() * factor
+        if c["fp8"]:
+            scale = c["k_scale"][g]
+            codes = (rows / scale).clamp(-448, 448).to(torch.float8_e4m3fn)
+            c["k_pool"][slots, g] = codes.view(torch.uint8)
+            c["k_values"][slots, g] = codes.double() * scale.double()
+        else:
+            c["k_pool"][slots, g] = rows.to(torch.bfloat16)   # k_values is the pool
+
+
+def chain_planted(c, targets):
+    """64-bit (out, lse, bound of out, bound of lse, weight of each row's planted key) of a
+    one-request chain of drafts after `plant`.
+
+    Bounds: a score is a sum of <= 128 exact products in fp32, off by e = 128 * 2^-24 of the
+    largest sum of |q k| scale, which moves a weight and the sum of weights by e each; an
+    accumulator rounds once per 16 keys, by 2^-23 of sum p |v| at most (the same for the sum
+    of weights); a weight is rounded to bf16 (2^-8) or f16 (2^-11), and one that f16 holds as
+    a subnormal or zero loses at most itself, all of them at most 1 - the planted key's
+    weight; out rounds to bf16 once."""
+    q = c["q"].double()
+    t, hq, d = q.shape
+    hkv = c["k_pool"].shape[1]
+    group = hq // hkv
+    slots = request_slots(c, 0)
+    n = slots.numel()
+    prior = n - t
+    step = 2.0 ** -11 if c["fp8"] else BF16_HALF
+    out, lse, tol, ltol, top = (torch.empty_like(q), q.new_empty(t, hq), torch.empty_like(q),
+                                q.new_empty(t, hq), [])
+    for g in range(hkv):
+        k, v = c["k_values"][slots, g].double(), c["v_values"][slots, g].double()
+        qr = q[:, g * group:(g + 1) * group].reshape(t * group, d)
+        s = qr @ k.T * c["scale"]
+        tok = torch.arange(t * group, device=q.device) // group
+        s = s.masked_fill(torch.arange(n, device=q.device)[None] > prior + tok[:, None], -math.inf)
+        e = 128 * 2.0 ** -24 * float((qr.abs() @ k.abs().T).max()) * c["scale"]
+        sums = 2 * n / 16 * 2.0 ** -23
+        l = torch.logsumexp(s, -1)
+        p = torch.exp(s - l[:, None])
+        o, mag = p @ v, p @ v.abs()
+        rows = torch.arange(len(targets), device=q.device)
+        w = p[rows, torch.tensor(targets, device=q.device)]
+        top.append(w)
+        b = BF16_HALF * o.abs() + (step + 2 * e + sums) * mag
+        if c["fp8"]:
+            b[:len(targets)] += (1 - w)[:, None] * v.abs().max()
+        heads = slice(g * group, (g + 1) * group)
+        out[:, heads], lse[:, heads] = o.view(t, group, d), l.view(t, group)
+        tol[:, heads], ltol[:, heads] = b.view(t, group, d), e + sums + 1e-4
+    return out, lse, tol, ltol, torch.cat(top)

@@ -352,3 +352,22 @@ def test_sizes_follow_a_refilled_descriptor(lib, monkeypatch):
     sa.seg_attn_tree_fp8(**{**large, **codes, **scales(4)})
     assert code_of(lambda: sa.seg_attn_tree_fp8(**{**large, **codes, **scales(2)})) == S["INVALID_ARG"]
     assert len(called) == 3
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_planted_keys_show_a_wrong_tile(fp8):
+    """The long-context check on the oracle alone: V rows of one K tile taken from another owned
+    tile leave the bounds in every row that looks into that tile, and in no other."""
+    rnd = random.Random(3)
+    draft, prior = 6, 4000
+    c = ref.tree_case(rnd, [draft], [prior], 8, 1, 128, fp8=fp8, device="cpu")
+    targets = rnd.sample(range(prior), draft * 8)
+    targets[:4] = [1280, 1290, 1407, 1408]
+    ref.plant(c, targets, 2.0)
+    want, _, tol, _, top = ref.chain_planted(c, targets)
+    assert float(top.min()) > 0.9
+    slots = ref.request_slots(c, 0)
+    c["v_values"][slots[1280:1408]] = c["v_values"][slots[256:384]].clone()
+    got = ref.chain_planted(c, targets)[0]
+    bad = ((got - want).abs() > tol).any(-1).flatten()
+    assert bad.tolist() == [1280 <= t < 1408 for t in targets]

@@ -530,3 +530,79 @@ def test_slots_past_two_to_the_31_values(fp8):
     for name in ("k_pool", "v_pool"):
         assert torch.equal(big[name][base:].view(kind), c[name].view(kind))
     assert sa.seg_attn_take_device_error() == 0
+
+
+def planted_positions(tab, seg_lens, prior, rnd):
+    """Logical keys where a wrong row would come from: one in every K tile (both parities, so
+    both softmax groups and every ring stage), the ends of every piece, and both sides of every
+    segment boundary at the distances where the copies' boxes of 32, 8 and 4 rows begin."""
+    p = tab.desc.pass_
+    work = tab.host[p.off_work: p.off_work + 16 * p.num_work].view(-1, 16)
+    pos = [i + rnd.randrange(128) for i in range(0, prior, 128)]
+    for w in work.tolist():
+        pos += [w[3] * 128, w[4] * 128 - 1]
+    at = 0
+    for l in seg_lens:
+        at += l
+        pos += [at + x for x in (-33, -32, -9, -8, -5, -4, -1, 0, 3, 4, 7, 8, 31, 32)]
+    pos = sorted({x for x in pos if 0 <= x < prior})
+    rnd.shuffle(pos)
+    return pos
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("draft,hq,hkv,d,factor", [(12, 16, 2, 128, 2.0),   # one query tile
+                                                   (40, 8, 1, 128, 2.0),    # two, and one
+                                                   (30, 4, 1, 64, 4.0)])
+def test_every_row_of_a_long_context_reaches_its_query(fp8, draft, hq, hkv, d, factor):
+    """Over 70,000 random keys one V row, or one tile of them, is lost in the sum.  Here every
+    (token, head) row looks at one planted key, whose V row is its output: a row read from the
+    wrong slot, tile or ring stage shows at full size.  A chain, so the plain prefill has to
+    give the same."""
+    rnd = random.Random(draft)
+    prior = 70000
+    c = ref.tree_case(rnd, [draft], [prior], hq, hkv, d, nseg=40, fp8=fp8)
+    tab = table(c)
+    plain = sa.SegTable.build([draft], c["seg_starts"], c["seg_lens"], c["num_slots"], True,
+                              sa.MODE_PREFILL, hq, hkv, d).to("cuda")
+    ws = torch.empty(max(16, plain.workspace_bytes), dtype=torch.uint8, device="cuda")
+    pos = planted_positions(tab, c["seg_lens"][0], prior, rnd)
+    assert tab.desc.pass_.num_work > 30 and len(c["seg_lens"][0]) > 10
+    rows = draft * hq // hkv
+    keep = c["k_pool"].clone(), c["k_values"].clone()
+    for at in range(0, len(pos), rows):
+        targets = pos[at:at + rows]
+        c["k_pool"].copy_(keep[0])
+        c["k_values"].copy_(keep[1])
+        ref.plant(c, targets, factor)
+        want, want_lse, tol, ltol, top = ref.chain_planted(c, targets)
+        assert float(top.min()) > 0.9
+        for what in ("tree", "prefill"):
+            if what == "tree":
+                out, lse = run(c, tab)
+            else:
+                out, lse = torch.full_like(c["q"], math.nan), torch.empty_like(lse)
+                args = (out, lse, plain.device, plain.desc, c["scale"], ws)
+                if fp8:
+                    sa.seg_attn_prefill_fp8(c["q"], c["k_pool"], c["v_pool"], c["k_scale"],
+                                            c["v_scale"], *args)
+                else:
+                    sa.seg_attn_prefill(c["q"], c["k_pool"], c["v_pool"], *args)
+            over = (out.double() - want).abs() / tol
+            assert float(over.max()) <= 1.0, (what, at, float(over.max()))
+            assert bool(((lse.double() - want_lse).abs() <= ltol).all()), (what, at)
+    assert sa.seg_attn_take_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("draft,hq,hkv,d", [(12, 16, 2, 128), (40, 8, 1, 128), (30, 4, 1, 64)])
+def test_scattered_keys_give_the_bits_of_contiguous_ones(fp8, draft, hq, hkv, d):
+    """The same 70,000 keys in 40 segments and in one run of slots: other copies, same arithmetic."""
+    rnd = random.Random(draft + 1)
+    c = ref.tree_case(rnd, [draft], [70000], hq, hkv, d, nseg=40, fp8=fp8)
+    parents = ref.random_parents(rnd, draft)
+    slots = ref.request_slots(c, 0)
+    flat = dict(c, seg_starts=[[0]], seg_lens=[[slots.numel()]], num_slots=slots.numel(),
+                k_pool=c["k_pool"][slots].contiguous(), v_pool=c["v_pool"][slots].contiguous())
+    (a, la), (b, lb) = (run(x, table(x, parents=parents)) for x in (c, flat))
+    assert bool(torch.isfinite(a).all()) and torch.equal(a, b) and torch.equal(la, lb)
