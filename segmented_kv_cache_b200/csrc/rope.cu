@@ -29,9 +29,10 @@ __device__ int g_rope_error;  // non-zero once a slot out of range was skipped
 
 namespace {
 
-// 128 threads with two units each: 88.8 us for 16381 tokens x 64 heads (6.0 TB/s, 0.92 of
-// the copy rate; 256 threads 91.5, 64 threads 90.8, one unit 99.7, four 95.0; warps that
-// own a token without a barrier 97, a persistent grid with the next loads in flight 94).
+// 128 threads with two units each: 84.0 us for 16381 tokens x 64 heads (6.4 TB/s, 0.98 of
+// the copy rate).  Measured beside an earlier form of 88.8 us: 256 threads 91.5, 64 threads
+// 90.8, one unit 99.7, four 95.0; warps that own a token without a barrier 97, a persistent
+// grid with the next loads in flight 94.
 constexpr int kRopeThreads = 128;
 constexpr int kScalarThreads = 256;
 constexpr int kUnit = 16;  // values per unit
@@ -66,7 +67,6 @@ struct RopeParams {
   int q_heads, kv_heads, head_dim, rotary;
   int head_units, token_units;     // units per head, per token
   FastDiv by_head, by_token;       // divisions by them
-  int cta_units, cta_tokens;       // units of one CTA, and the most tokens they touch
   float amp, sign;                 // sign -1: the transposed rotation
   uint64_t turns[SEG_ATTN_ROPE_MAX_PAIRS];
 };
@@ -153,128 +153,124 @@ __device__ __forceinline__ Unit locate(const RopeParams& p, int64_t t0, uint32_t
   return x;
 }
 
-// NI: units per thread and pass.  A CTA's units are a multiple of kRopeThreads * NI
-// or the whole call.
+// NI: units per thread.
 template <bool INTERLEAVED, bool FP8, int NI>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   // [tokens of this CTA][8][rotary / 16]: pair 8 u + e of a token at e * (rotary / 16) + u,
   // so that the units u of neighbouring lanes read neighbouring values
   extern __shared__ float2 cs[];
-  const uint32_t first = blockIdx.x * (uint32_t)p.cta_units;  // a launch has < 2^31 units
-  const int count = (int)min((uint32_t)p.cta_units, (uint32_t)p.n_tokens * p.token_units - first);
+  constexpr uint32_t kCtaUnits = kRopeThreads * NI;
+  const uint32_t first = blockIdx.x * kCtaUnits;  // a launch has < 2^31 units
+  const int count = (int)min(kCtaUnits, (uint32_t)p.n_tokens * p.token_units - first);
   const uint32_t t0 = p.by_token(first);
   const int off0 = (int)(first - t0 * p.token_units);
   const int pairs = p.rotary / 2, rot_units = p.rotary / kUnit;
 
-  for (int base = 0; base < count; base += kRopeThreads * NI) {
-    uint4 a[NI], b[NI];
-    Unit un[NI];
-    int32_t slot[NI];
+  uint4 a[NI], b[NI];
+  Unit un[NI];
+  int32_t slot[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int at = base + i * kRopeThreads + threadIdx.x;
-      un[i].kind = -1;
-      if (at >= count) continue;
-      un[i] = locate(p, t0, off0 + at);
-      const Unit& x = un[i];
-      const __nv_bfloat16* row =
-          (x.kind == 0   ? p.q + x.token * p.q_stride
-           : x.kind == 1 ? p.k + x.token * p.k_stride
-                         : p.v + x.token * p.v_stride) + x.head * p.head_dim;
-      const bool split = !INTERLEAVED && x.kind != 2 && x.u < rot_units;
-      const int ca = split ? 8 * x.u : kUnit * x.u;
-      a[i] = *reinterpret_cast<const uint4*>(row + ca);
-      b[i] = *reinterpret_cast<const uint4*>(row + (split ? ca + pairs : ca + 8));
-      if (x.kind != 0) slot[i] = __ldg(p.slots + x.token);
-    }
-    if (base == 0) {
-      const int tokens = (int)p.by_token(off0 + count - 1) + 1;
-      for (int i = threadIdx.x; i < tokens * pairs; i += kRopeThreads) {
-        const int t = i / pairs, j = i - t * pairs;
-        cs[t * pairs + (j & 7) * rot_units + (j >> 3)] =
-            cos_sin(p.turns[j], __ldg(p.positions + t0 + t), p.amp, p.sign);
-      }
-      __syncthreads();
-    }
+  for (int i = 0; i < NI; ++i) {
+    const int at = i * kRopeThreads + threadIdx.x;
+    un[i].kind = -1;
+    if (at >= count) continue;
+    un[i] = locate(p, t0, off0 + at);
+    const Unit& x = un[i];
+    const __nv_bfloat16* row =
+        (x.kind == 0   ? p.q + x.token * p.q_stride
+         : x.kind == 1 ? p.k + x.token * p.k_stride
+                       : p.v + x.token * p.v_stride) + x.head * p.head_dim;
+    const bool split = !INTERLEAVED && x.kind != 2 && x.u < rot_units;
+    const int ca = split ? 8 * x.u : kUnit * x.u;
+    a[i] = *reinterpret_cast<const uint4*>(row + ca);
+    b[i] = *reinterpret_cast<const uint4*>(row + (split ? ca + pairs : ca + 8));
+    if (x.kind != 0) slot[i] = __ldg(p.slots + x.token);
+  }
+  const int tokens = (int)p.by_token(off0 + count - 1) + 1;
+  for (int i = threadIdx.x; i < tokens * pairs; i += kRopeThreads) {
+    const int t = i / pairs, j = i - t * pairs;
+    cs[t * pairs + (j & 7) * rot_units + (j >> 3)] =
+        cos_sin(p.turns[j], __ldg(p.positions + t0 + t), p.amp, p.sign);
+  }
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const Unit& x = un[i];
-      if (x.kind < 0) continue;
-      const bool rot = x.kind != 2 && x.u < rot_units;
-      const bool split = !INTERLEAVED && rot;
-      const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-      const uint32_t wb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-      // the unit's values: first sides f, second sides g of pairs (2 e, 2 e + 1)
-      float2 f[4], g[4];
-      const float2* c = cs + (int)(x.token - t0) * pairs + x.u;
+  for (int i = 0; i < NI; ++i) {
+    const Unit& x = un[i];
+    if (x.kind < 0) continue;
+    const bool rot = x.kind != 2 && x.u < rot_units;
+    const bool split = !INTERLEAVED && rot;
+    const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+    const uint32_t wb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+    // the unit's values: first sides f, second sides g of pairs (2 e, 2 e + 1)
+    float2 f[4], g[4];
+    const float2* c = cs + (int)(x.token - t0) * pairs + x.u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (INTERLEAVED) {
-          const uint32_t w0 = e < 2 ? wa[2 * e] : wb[2 * e - 4];
-          const uint32_t w1 = e < 2 ? wa[2 * e + 1] : wb[2 * e - 3];
-          f[e] = make_float2(bf_lo(w0), bf_lo(w1));
-          g[e] = make_float2(bf_hi(w0), bf_hi(w1));
-        } else {
-          f[e] = make_float2(bf_lo(wa[e]), bf_hi(wa[e]));
-          g[e] = make_float2(bf_lo(wb[e]), bf_hi(wb[e]));
-        }
-        if (rot) {
-          const float2 p0 = c[2 * e * rot_units], p1 = c[(2 * e + 1) * rot_units];
-          const uint64_t cc = pack2(p0.x, p1.x);
-          const uint64_t f2 = pack2(f[e].x, f[e].y), g2 = pack2(g[e].x, g[e].y);
-          f[e] = unpack2(fma2(g2, pack2(-p0.y, -p1.y), mul2(f2, cc)));
-          g[e] = unpack2(fma2(f2, pack2(p0.y, p1.y), mul2(g2, cc)));
-        }
-      }
-      uint4 oa = a[i], ob = b[i];  // what is not turned keeps its bits
-      if (rot && (x.kind == 0 || !FP8)) {
-        if (INTERLEAVED) {
-          oa = make_uint4(bf_pack(f[0].x, g[0].x), bf_pack(f[0].y, g[0].y),
-                          bf_pack(f[1].x, g[1].x), bf_pack(f[1].y, g[1].y));
-          ob = make_uint4(bf_pack(f[2].x, g[2].x), bf_pack(f[2].y, g[2].y),
-                          bf_pack(f[3].x, g[3].x), bf_pack(f[3].y, g[3].y));
-        } else {
-          oa = make_uint4(bf_pack(f[0].x, f[0].y), bf_pack(f[1].x, f[1].y),
-                          bf_pack(f[2].x, f[2].y), bf_pack(f[3].x, f[3].y));
-          ob = make_uint4(bf_pack(g[0].x, g[0].y), bf_pack(g[1].x, g[1].y),
-                          bf_pack(g[2].x, g[2].y), bf_pack(g[3].x, g[3].y));
-        }
-      }
-      const int ca = split ? 8 * x.u : kUnit * x.u, cb = split ? ca + pairs : ca + 8;
-      if (x.kind == 0) {
-        __nv_bfloat16* row = p.q_out + x.token * p.q_out_stride + x.head * p.head_dim;
-        *reinterpret_cast<uint4*>(row + ca) = oa;
-        *reinterpret_cast<uint4*>(row + cb) = ob;
-        continue;
-      }
-      if (slot[i] < 0 || slot[i] >= p.num_slots) {
-        if (x.head == 0 && x.u == 0) atomicOr(&g_rope_error, 1);
-        continue;
-      }
-      const int64_t at = ((int64_t)slot[i] * p.kv_heads + x.head) * p.head_dim;
-      void* pool = x.kind == 1 ? p.k_pool : p.v_pool;
-      if (FP8) {
-        const float sc = __ldg((x.kind == 1 ? p.k_scale : p.v_scale) + x.head), rc = 1.f / sc;
-        uint8_t* row = static_cast<uint8_t*>(pool) + at;
-        uint2 qa, qb;
-        if (INTERLEAVED) {
-          qa = make_uint2(quant4(f[0].x, g[0].x, f[0].y, g[0].y, sc, rc),
-                          quant4(f[1].x, g[1].x, f[1].y, g[1].y, sc, rc));
-          qb = make_uint2(quant4(f[2].x, g[2].x, f[2].y, g[2].y, sc, rc),
-                          quant4(f[3].x, g[3].x, f[3].y, g[3].y, sc, rc));
-        } else {
-          qa = make_uint2(quant4(f[0].x, f[0].y, f[1].x, f[1].y, sc, rc),
-                          quant4(f[2].x, f[2].y, f[3].x, f[3].y, sc, rc));
-          qb = make_uint2(quant4(g[0].x, g[0].y, g[1].x, g[1].y, sc, rc),
-                          quant4(g[2].x, g[2].y, g[3].x, g[3].y, sc, rc));
-        }
-        *reinterpret_cast<uint2*>(row + ca) = qa;
-        *reinterpret_cast<uint2*>(row + cb) = qb;
+    for (int e = 0; e < 4; ++e) {
+      if (INTERLEAVED) {
+        const uint32_t w0 = e < 2 ? wa[2 * e] : wb[2 * e - 4];
+        const uint32_t w1 = e < 2 ? wa[2 * e + 1] : wb[2 * e - 3];
+        f[e] = make_float2(bf_lo(w0), bf_lo(w1));
+        g[e] = make_float2(bf_hi(w0), bf_hi(w1));
       } else {
-        __nv_bfloat16* row = static_cast<__nv_bfloat16*>(pool) + at;
-        *reinterpret_cast<uint4*>(row + ca) = oa;
-        *reinterpret_cast<uint4*>(row + cb) = ob;
+        f[e] = make_float2(bf_lo(wa[e]), bf_hi(wa[e]));
+        g[e] = make_float2(bf_lo(wb[e]), bf_hi(wb[e]));
       }
+      if (rot) {
+        const float2 p0 = c[2 * e * rot_units], p1 = c[(2 * e + 1) * rot_units];
+        const uint64_t cc = pack2(p0.x, p1.x);
+        const uint64_t f2 = pack2(f[e].x, f[e].y), g2 = pack2(g[e].x, g[e].y);
+        f[e] = unpack2(fma2(g2, pack2(-p0.y, -p1.y), mul2(f2, cc)));
+        g[e] = unpack2(fma2(f2, pack2(p0.y, p1.y), mul2(g2, cc)));
+      }
+    }
+    uint4 oa = a[i], ob = b[i];  // what is not turned keeps its bits
+    if (rot && (x.kind == 0 || !FP8)) {
+      if (INTERLEAVED) {
+        oa = make_uint4(bf_pack(f[0].x, g[0].x), bf_pack(f[0].y, g[0].y),
+                        bf_pack(f[1].x, g[1].x), bf_pack(f[1].y, g[1].y));
+        ob = make_uint4(bf_pack(f[2].x, g[2].x), bf_pack(f[2].y, g[2].y),
+                        bf_pack(f[3].x, g[3].x), bf_pack(f[3].y, g[3].y));
+      } else {
+        oa = make_uint4(bf_pack(f[0].x, f[0].y), bf_pack(f[1].x, f[1].y),
+                        bf_pack(f[2].x, f[2].y), bf_pack(f[3].x, f[3].y));
+        ob = make_uint4(bf_pack(g[0].x, g[0].y), bf_pack(g[1].x, g[1].y),
+                        bf_pack(g[2].x, g[2].y), bf_pack(g[3].x, g[3].y));
+      }
+    }
+    const int ca = split ? 8 * x.u : kUnit * x.u, cb = split ? ca + pairs : ca + 8;
+    if (x.kind == 0) {
+      __nv_bfloat16* row = p.q_out + x.token * p.q_out_stride + x.head * p.head_dim;
+      *reinterpret_cast<uint4*>(row + ca) = oa;
+      *reinterpret_cast<uint4*>(row + cb) = ob;
+      continue;
+    }
+    if (slot[i] < 0 || slot[i] >= p.num_slots) {
+      if (x.head == 0 && x.u == 0) atomicOr(&g_rope_error, 1);
+      continue;
+    }
+    const int64_t at = ((int64_t)slot[i] * p.kv_heads + x.head) * p.head_dim;
+    void* pool = x.kind == 1 ? p.k_pool : p.v_pool;
+    if (FP8) {
+      const float sc = __ldg((x.kind == 1 ? p.k_scale : p.v_scale) + x.head), rc = 1.f / sc;
+      uint8_t* row = static_cast<uint8_t*>(pool) + at;
+      uint2 qa, qb;
+      if (INTERLEAVED) {
+        qa = make_uint2(quant4(f[0].x, g[0].x, f[0].y, g[0].y, sc, rc),
+                        quant4(f[1].x, g[1].x, f[1].y, g[1].y, sc, rc));
+        qb = make_uint2(quant4(f[2].x, g[2].x, f[2].y, g[2].y, sc, rc),
+                        quant4(f[3].x, g[3].x, f[3].y, g[3].y, sc, rc));
+      } else {
+        qa = make_uint2(quant4(f[0].x, f[0].y, f[1].x, f[1].y, sc, rc),
+                        quant4(f[2].x, f[2].y, f[3].x, f[3].y, sc, rc));
+        qb = make_uint2(quant4(g[0].x, g[0].y, g[1].x, g[1].y, sc, rc),
+                        quant4(g[2].x, g[2].y, g[3].x, g[3].y, sc, rc));
+      }
+      *reinterpret_cast<uint2*>(row + ca) = qa;
+      *reinterpret_cast<uint2*>(row + cb) = qb;
+    } else {
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(pool) + at;
+      *reinterpret_cast<uint4*>(row + ca) = oa;
+      *reinterpret_cast<uint4*>(row + cb) = ob;
     }
   }
 }
@@ -359,16 +355,16 @@ int launch(RopeParams& p, bool vectors, cudaStream_t st) {
   // two units in flight per thread in long calls, one in short ones, where latency counts
   // (128 tokens of 64 + 8 + 8 heads 3.0 against 3.3 us; 3000 x 32 heads 11.9 against 11.4)
   const int ni = all * p.token_units >= (int64_t)kSmCount * 8 * kRopeThreads * 2 ? 2 : 1;
-  p.cta_units = kRopeThreads * ni;
-  p.cta_tokens = (p.cta_units - 1) / p.token_units + 2;
-  // at most 34 KB: a token has at least rotary / 16 units
-  const size_t smem = (size_t)p.cta_tokens * (p.rotary / 2) * sizeof(float2);
+  const int cta_units = kRopeThreads * ni;
+  const int cta_tokens = (cta_units - 1) / p.token_units + 2;  // the most that a CTA touches
+  // at most 18.2 KB: a token has at least rotary / 16 units
+  const size_t smem = (size_t)cta_tokens * (p.rotary / 2) * sizeof(float2);
   // a launch counts its units in 31 bits: more tokens take several
-  const int64_t most = (INT32_MAX - p.cta_units) / p.token_units;
+  const int64_t most = (INT32_MAX - cta_units) / p.token_units;
   for (int64_t done = 0; done < all; done += p.n_tokens) {
     p.n_tokens = std::min(all - done, most);
     const unsigned blocks =
-        (unsigned)((p.n_tokens * p.token_units + p.cta_units - 1) / p.cta_units);
+        (unsigned)((p.n_tokens * p.token_units + cta_units - 1) / cta_units);
     if (ni == 2)
       rope_kernel<INTERLEAVED, FP8, 2><<<blocks, kRopeThreads, smem, st>>>(p);
     else
