@@ -606,3 +606,80 @@ def test_scattered_keys_give_the_bits_of_contiguous_ones(fp8, draft, hq, hkv, d)
                 k_pool=c["k_pool"][slots].contiguous(), v_pool=c["v_pool"][slots].contiguous())
     (a, la), (b, lb) = (run(x, table(x, parents=parents)) for x in (c, flat))
     assert bool(torch.isfinite(a).all()) and torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_captured_behind_copies_and_a_join_of_streams():
+    """The pass is a programmatic dependent of a kernel before it; behind a copy, and behind two
+    streams that join, it has to wait for all of them.  Replays with other inputs and another
+    table (copied inside the graph) give the eager calls' bits, row moves included."""
+    rnd = random.Random(30)
+    hq, hk, d = 16, 2, 128
+    base = ref.tree_case(rnd, [6, 9], [3000, 700], hq, hk, d)
+    forms = [[p for t in base["draft"] for p in ref.random_parents(rnd, t)] for _ in range(4)]
+    tabs = [table(base, parents=f) for f in forms]
+    assert tabs[0].desc.pass_.num_merge > 0
+    assert len({t.desc.table_bytes for t in tabs}) == 1   # the same plan, other masks
+    slots = [ref.request_slots(base, r)[-t:].to(torch.int32) for r, t in enumerate(base["draft"])]
+    at = torch.cat(slots)
+    dev_table = torch.zeros_like(tabs[0].device)
+    host_table = torch.empty_like(tabs[0].host, pin_memory=True)
+    q, new = torch.empty_like(base["q"]), torch.empty(15, hk, d, dtype=torch.bfloat16, device="cuda")
+    host_q, host_new = (torch.empty(t.shape, dtype=t.dtype, pin_memory=True) for t in (q, new))
+    kp, vp = base["k_pool"].clone(), base["v_pool"].clone()
+    out, lse = torch.empty_like(q), torch.empty(15, hq, device="cuda")
+    ws = torch.empty(tabs[0].workspace_bytes, dtype=torch.uint8, device="cuda")
+    src, dst = at[[1, 3]].clone(), at[[0, 2]].clone()
+
+    def step(side=None):
+        q.copy_(host_q, non_blocking=True)
+        if side is not None:
+            side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            new.copy_(host_new, non_blocking=True)
+            sa.seg_attn_kv_append(new, new, at, kp, vp)
+        dev_table.copy_(host_table, non_blocking=True)
+        if side is not None:
+            torch.cuda.current_stream().wait_stream(side)
+        sa.seg_attn_tree(q, kp, vp, out, lse, dev_table, tabs[0].desc, base["scale"], ws)
+        sa.seg_attn_kv_move(kp, vp, src, dst)
+
+    def inputs(k):
+        g = torch.Generator().manual_seed(100 + k)
+        host_q.copy_(torch.randn(q.shape, generator=g))
+        host_new.copy_(torch.randn(new.shape, generator=g))
+        host_table.copy_(tabs[k].host)
+
+    inputs(0)
+    step()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        step(side)
+    for k in range(4):
+        inputs(k)
+        kp.copy_(base["k_pool"])
+        vp.copy_(base["v_pool"])
+        step()
+        torch.cuda.synchronize()
+        want = [x.clone() for x in (out, lse, kp, vp)]
+        kp.copy_(base["k_pool"])
+        vp.copy_(base["v_pool"])
+        out.fill_(math.nan)
+        lse.fill_(math.nan)
+        torch.cuda.synchronize()
+        graph.replay()
+        graph.replay()   # twice in a row: the second call's pass behind the first one's move
+        torch.cuda.synchronize()
+        for a, b in zip((out, lse), want):
+            assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+        for a, b in zip((kp, vp), want[2:]):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        c = dict(base, q=q)
+        if k == 3:   # and they are right, not only alike: the cache before its rows moved
+            kv = base["k_pool"].clone(), base["v_pool"].clone()
+            for x in kv:
+                x[at.long()] = new
+            ref.check_tree(out, lse, ref.tree(q, kv[0], kv[1], c["draft"],
+                                              ref.visible(c["draft"], parents=forms[k]),
+                                              c["seg_starts"], c["seg_lens"], c["scale"]))
+    assert sa.seg_attn_take_device_error() == 0
