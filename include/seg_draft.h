@@ -155,6 +155,11 @@ int seg_attn_rope_append_fp8(const void* q, int64_t q_stride, void* q_out, int64
  *   mask        [sum draft_lens[r]^2] bytes, per request row-major: i sees j
  *               where the byte is not 0 (a token need not see itself)
  *   neither     a chain: i sees 0 .. i
+ * Scores, their maximum and sum and the output are accumulated in fp32.  A
+ * softmax weight is rounded to the 16-bit operand of its product with V: bf16
+ * over a bf16 cache (2^-8 of the weight), f16 over an E4M3 cache (2^-11; queries
+ * are f16 there too, so |q| must be below 65504).  The sum divides by the
+ * unrounded weights, and out rounds to bf16 once.
  * out and lse as in seg_attn.h; a token that sees no key (P_r = 0 and an empty
  * mask row) gets out = 0 and lse = -inf.  What a token does not see, NaN and
  * infinities included, never reaches its row.

@@ -14,10 +14,14 @@ namespace segattn {
 using Row8 = std::array<int32_t, 8>;
 using Row4 = std::array<int32_t, 4>;
 // prefill piece: request, kv head, first query, first K tile | end K tile, partial
-// slot (-1: none), one-tile flag, end of the request's segments | first packed query
+// slot (-1: none), flag (below), end of the request's segments | first packed query
 // row, queries and keys of the request, segment holding the piece's first key | pool
 // slot of the piece's first key when its first K tile lies inside that segment (-1:
-// it does not), three zero words
+// it does not), three words: zero, in a tree table the table's first mask word of the
+// request (low and high half) and zero.
+// Flag.  Plain tables: the piece belongs to the launch of the one-tile kernel (all pieces
+// of a pass, or none).  Tree tables, which launch one kernel for all pieces: the item has
+// queries in its first query tile only, and both softmax groups take that tile.
 constexpr int kWorkInts = 16;
 using Row16 = std::array<int32_t, kWorkInts>;
 

@@ -42,8 +42,9 @@
 // the QK that refills an S buffer never overwrites what the PV before it reads.
 // TMEM columns: O [0,128) P0 [128,192) P1 [192,256) S0 [256,384) S1 [384,512).
 // Over an FP8 cache the last two warps widen the E4M3 codes of K and of V tiles to f16
-// in place, inside the ring slot whose second half the codes were loaded into.  (A single staging tile per K and V, as the one-tile kernel had, exposed every tile's
-// load latency: 64 trees of 16 over 4k keys, 308 us; now 200.)
+// in place, inside the ring slot whose second half the codes were loaded into.  (A single
+// staging tile per K and V, as the one-tile kernel had, exposed every tile's load latency:
+// 64 trees of 16 over 4k keys, 308 us; now 206.)
 // Drafted tokens (TREE, see the kernel's comment): masks of bits on the last K tiles, and
 // items of one query tile run both softmax groups on it.
 // Every mbarrier wait is bounded (1 s); a timeout stops all roles of the CTA,
@@ -938,10 +939,12 @@ __global__ void __launch_bounds__(cta_threads<SINGLE, FP8>(), 1)
         rescale = true;
       }
       const float base = m_ref == -INFINITY ? 0.f : m_ref * sl2;
-      // P = 2^(s*scale*log2e - base), packed in pairs (bf16, or f16 over an FP8 cache).
-      // Queries in TMEM: f32x2 pairs for the scale-and-subtract and the sums (fewer
-      // instructions per score); the P-over-S variants keep scalar arithmetic, whose
-      // register allocation does not spill.
+      // P = 2^(s*scale*log2e - base), packed in pairs: bf16, or f16 over an FP8 cache (V is
+      // widened to f16 there).  The one rounding of a weight, by at most 2^-8 or 2^-11 of
+      // it, is the price of the tensor cores' 16-bit operand; the sum l takes the unrounded
+      // ones.  Two tiles: f32x2 pairs for the scale-and-subtract and the sums (fewer
+      // instructions per score); the one-tile kernel keeps scalar arithmetic, whose register
+      // allocation does not spill.
       uint64_t ls = f2_pack(0.f, 0.f);
       float ls0 = 0.f, ls1 = 0.f;
       const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);

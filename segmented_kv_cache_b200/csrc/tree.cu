@@ -42,8 +42,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams p) {
   const int tok0 = __ldg(p.tab.q_offsets + req);
   const int q_len = __ldg(p.tab.q_offsets + req + 1) - tok0;
   const int lane = threadIdx.x & 31, gi = lane >> 3, l8 = lane & 7;
-  // launched as a programmatic dependent of the prefill pass: what precedes this line
-  // overlaps its end, what follows reads the partials
+  // launched as a programmatic dependent of the prefill pass, which gives no early trigger:
+  // this grid starts once the pass's CTAs have exited (the launch itself is hidden), and
+  // what follows reads the partials
   ptx::grid_dependency_wait();
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int qi = q0 + (row / kTileRows) * p.qpt + (row % kTileRows) / p.group;

@@ -22,15 +22,17 @@ namespace {
 using namespace segattn;
 
 // Costs in tenths of the time a K tile of an item with one query tile takes (1.34 us: a
-// bf16 cache's bytes at one SM's share of memory).  A K tile of an item with two query
-// tiles takes 1.9 us (its softmax).  A piece: start-up, first scores, drain and epilogue,
-// 7 us measured.  A merge: its launch, and per piece the partial written and read back
-// (128 rows x 512 bytes each way per query tile).
+// bf16 cache's bytes at one SM's share of memory, d = 128).  A K tile of an item with two
+// query tiles takes 1.9 us (its softmax).  A piece: start-up, first scores, drain and
+// epilogue, 7 us measured.  A merge: its launch, and per piece the partial written and read
+// back (128 rows x 512 bytes each way per query tile).  A table serves either cache, so
+// E4M3 caches are cut by the same costs (there a K tile of both kinds of item is bound by
+// its softmax: 1.6 and 1.9 us), and so are heads of 64.
 constexpr int64_t kTileCost = 10, kTwoTileCost = 14, kPieceCost = 50;
 constexpr double kMergeCost = 20.0, kMergePartCost = 0.23;
 // The uncut plan is taken when it is this near the best: while memory bounds the pass,
 // idle SMs cost less than the simulation says (32 trees of 16 over 8k keys: uncut 186 us,
-// the plan simulated 4 % shorter 201).
+// a plan simulated 4 % shorter 201; one measurement, with every K tile costed alike).
 constexpr double kUncutSlack = 1.08;
 
 // Where to cut the items along their keys: the cuts whose simulated schedule (pieces
@@ -291,7 +293,8 @@ int build(int batch, const int32_t* draft_lens, const int32_t* parents, const ui
   fill_request_words(pieces.work, q_off, keys, own, seg_off);
   for (size_t i = 0; i < pieces.work.size(); ++i) {
     const int64_t at = desc->off_mask + mask_at[pieces.work[i][0]];
-    // one-tile items: both softmax groups take their one query tile
+    // both softmax groups take the one query tile of such an item.  Set here, after
+    // emit_pieces has ordered the pieces longest first: one launch runs both kinds.
     pieces.work[i][6] = q_off[pieces.work[i][0] + 1] - q_off[pieces.work[i][0]] - pieces.work[i][2] <= qpt;
     pieces.work[i][13] = (int32_t)(uint32_t)(at & 0xffffffff);
     pieces.work[i][14] = (int32_t)(at >> 32);
