@@ -29,10 +29,10 @@ __device__ int g_rope_error;  // non-zero once a slot out of range was skipped
 
 namespace {
 
-// 128 threads with two units each: 84.0 us for 16381 tokens x 64 heads (6.4 TB/s, 0.98 of
-// the copy rate).  Measured beside an earlier form of 88.8 us: 256 threads 91.5, 64 threads
-// 90.8, one unit 99.7, four 95.0; warps that own a token without a barrier 97, a persistent
-// grid with the next loads in flight 94.
+// 128 threads with two units each: 83.8 us for 16381 tokens x 64 heads (6.4 TB/s, 0.98 of
+// the copy rate), one unit 93.1.  Measured beside an earlier form of 88.8 us: 256 threads
+// 91.5, 64 threads 90.8, four units 95.0; warps that own a token without a barrier 97, a
+// persistent grid with the next loads in flight 94.
 constexpr int kRopeThreads = 128;
 constexpr int kScalarThreads = 256;
 constexpr int kUnit = 16;  // values per unit
@@ -353,7 +353,8 @@ int launch(RopeParams& p, bool vectors, cudaStream_t st) {
   p.by_token = fast_div(p.token_units);
   const int64_t all = p.n_tokens;
   // two units in flight per thread in long calls, one in short ones, where latency counts
-  // (128 tokens of 64 + 8 + 8 heads 3.0 against 3.3 us; 3000 x 32 heads 11.9 against 11.4)
+  // (one unit against two, us: one token 2.6 / 3.1, 128 tokens of 64 + 8 + 8 heads 3.0 / 3.3,
+  // 1024 of them 9.0 / 8.3, 16381 tokens of 64 heads 93.1 / 83.8)
   const int ni = all * p.token_units >= (int64_t)kSmCount * 8 * kRopeThreads * 2 ? 2 : 1;
   const int cta_units = kRopeThreads * ni;
   const int cta_tokens = (cta_units - 1) / p.token_units + 2;  // the most that a CTA touches
